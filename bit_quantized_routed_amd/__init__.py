@@ -24,6 +24,9 @@ ACT_F32, ACT_BF16 = 0, 1
 PATH_ROUTE, PATH_DECODE, PATH_PREFILL, PATH_LAYER_DECODE = 0, 1, 2, 3
 LAYER_TOKENWISE_DECODE = 1
 LAYER_ONE_STREAM = 2
+SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
+ROUTER_RENORM = 1
+Q8_SWIGLU = 1
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED",
           -3: "MOE_ERR_WORKSPACE", -4: "MOE_ERR_HIP"}
 BLOCK_BYTES = {FMT_CB2: 38, FMT_Q2K: 84, FMT_Q4K: 144, FMT_Q5K: 176, FMT_Q6K: 210, FMT_CB2S: 66}
@@ -58,6 +61,25 @@ class ExpertCacheC(ctypes.Structure):
                 ("ctl", ctypes.c_void_p), ("stats", ctypes.c_void_p)]
 
 
+class RouterC(ctypes.Structure):
+    """struct moe_router (host struct of device pointers)."""
+    _fields_ = [("hidden", ctypes.c_int32), ("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("n_groups", ctypes.c_int32), ("keep_groups", ctypes.c_int32),
+                ("flags", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("w_router", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class NormC(ctypes.Structure):
+    """struct moe_norm."""
+    _fields_ = [("hidden", ctypes.c_int32), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p)]
+
+
+class LinearC(ctypes.Structure):
+    """struct moe_linear."""
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("ldw", ctypes.c_int64),
+                ("w", ctypes.c_void_p), ("w_scale", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
 class Profile(ctypes.Structure):
     """struct moe_profile: bracket launch number `kernel` with two hipEvents."""
     _fields_ = [("kernel", ctypes.c_int32), ("n_launches", ctypes.c_int32),
@@ -70,7 +92,8 @@ _lib = None
 EXPORTS = ["moe_route", "moe_expert_ffn_decode", "moe_expert_ffn_prefill", "q2_pack", "q2_unpack",
            "q2_packed_bytes", "moe_workspace_bytes", "moe_status_str", "moe_last_error",
            "moe_expert_ffn_decode_noalloc", "moe_layer_decode", "moe_expert_cache_bytes", "moe_expert_cache_init",
-           "moe_expert_cache_map", "moe_expert_cache_prefetch"]
+           "moe_expert_cache_map", "moe_expert_cache_prefetch", "moe_route_scored", "moe_route_scored_workspace_bytes",
+           "moe_residual_norm", "moe_quant_i8", "moe_linear_i8", "moe_linear_i8_workspace_bytes"]
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 # measurement kernels the benchmark uses (csrc/moe_probe.h; not part of the layer's ABI)
 PROBE_EXPORTS = ["moe_probe_stream_read", "moe_probe_mfma_loop"]
@@ -116,6 +139,19 @@ def lib():
     L.moe_expert_cache_map.restype = i32
     L.moe_expert_cache_prefetch.argtypes = [cp, i32, lp, vp, i32, vp]
     L.moe_expert_cache_prefetch.restype = i32
+    rp, np_, wp = ctypes.POINTER(RouterC), ctypes.POINTER(NormC), ctypes.POINTER(LinearC)
+    L.moe_route_scored.argtypes = [rp, vp, i32, i64, i32, vp, vp, vp, vp, vp, vp, sz, vp, pp]
+    L.moe_route_scored.restype = i32
+    L.moe_route_scored_workspace_bytes.argtypes = [rp, i32]
+    L.moe_route_scored_workspace_bytes.restype = sz
+    L.moe_residual_norm.argtypes = [np_, i32, vp, i32, i64, vp, i32, i64, vp, i64, vp, i32, i64, vp, i64, vp, vp, pp]
+    L.moe_residual_norm.restype = i32
+    L.moe_quant_i8.argtypes = [vp, i32, i64, i32, i32, i32, vp, i64, vp, vp, pp]
+    L.moe_quant_i8.restype = i32
+    L.moe_linear_i8.argtypes = [wp, i32, vp, i64, vp, vp, i64, vp, i32, i64, vp, sz, vp, pp]
+    L.moe_linear_i8.restype = i32
+    L.moe_linear_i8_workspace_bytes.argtypes = [wp, i32]
+    L.moe_linear_i8_workspace_bytes.restype = sz
     L.moe_probe_stream_read.argtypes = [vp, sz, i32, i32, vp, vp]
     L.moe_probe_stream_read.restype = i32
     L.moe_probe_mfma_loop.argtypes = [i32, i32, i32, vp, vp]
@@ -359,3 +395,164 @@ class ExpertCache:
     def key_of(self):
         import torch
         return self._field(self.c.key_of, self.c.n_slots, torch.int32)
+
+
+# ------------------------------------------------------------------ around the experts
+def _act(t, what: str) -> int:
+    """Activation type of a tensor of rows: fp32 or bf16, elements of a row adjacent."""
+    import torch
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError("%s: rows of adjacent elements are needed, got shape %s, strides %s"
+                         % (what, tuple(t.shape), t.stride()))
+    if t.dtype == torch.float32:
+        return ACT_F32
+    if t.dtype == torch.bfloat16:
+        return ACT_BF16
+    raise ValueError("%s: fp32 or bf16 is needed, got %s" % (what, t.dtype))
+
+
+def _vector(t, n: int, what: str):
+    import torch
+    if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous()):
+        raise ValueError("%s: %d contiguous fp32 values are needed" % (what, n))
+    return t
+
+
+def _shaped(t, shape, what: str):
+    if t is not None and t.shape != shape:
+        raise ValueError("%s: shape %s is needed, got %s" % (what, tuple(shape), tuple(t.shape)))
+    return t
+
+
+def _codes(t, shape, what: str):
+    """Rows of int8 codes, elements of a row adjacent."""
+    import torch
+    if t.dtype != torch.int8 or t.shape != shape or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError("%s: int8 rows of shape %s are needed" % (what, tuple(shape)))
+    return t
+
+
+def _readable(t, what: str):
+    """moe_linear_i8 reads each row up to the next multiple of 16 bytes: the last row must have them."""
+    T, K = t.shape
+    if T and t.storage_offset() + (T - 1) * t.stride(0) + (K + 15) // 16 * 16 > t.untyped_storage().nbytes():
+        raise ValueError("%s: the last row has no room up to a multiple of 16 bytes (see empty_i8)" % what)
+    return t
+
+
+def empty_i8(T: int, K: int, device="cuda"):
+    """Rows for int8 codes [T, K] at a stride of a multiple of 16 bytes, as linear_i8 takes them."""
+    import torch
+    return torch.empty((T, (K + 15) // 16 * 16), dtype=torch.int8, device=device)[:, :K]
+
+
+class NormWeights:
+    """The weight and epsilon of one residual norm."""
+
+    def __init__(self, weight, eps: float = 1e-6):
+        self.weight = _vector(weight, weight.shape[0], "weight")
+        self.hidden = weight.shape[0]
+        self.c = NormC(self.hidden, eps, _ptr(weight))
+
+
+def residual_norm(w: NormWeights, x, residual=None, total=None, out=None, q=None, q_scale=None, stream=None, prof=None):
+    """s = x + residual (kept in `total`, which may be `residual`), its norm as `out` and / or as codes q with q_scale."""
+    T, H = x.shape
+    shape = (T, w.hidden)
+    ax = _act(_shaped(x, shape, "x"), "x")
+    ar = ao = 0
+    ldr = lds = ldo = ldq = 0
+    if residual is not None:
+        ar, ldr = _act(_shaped(residual, shape, "residual"), "residual"), residual.stride(0)
+    if total is not None:
+        lds = total.stride(0)
+        if residual is None or _act(_shaped(total, shape, "total"), "total") != ar:
+            raise ValueError("total: needs a residual, and its type")
+    if out is not None:
+        ao, ldo = _act(_shaped(out, shape, "out"), "out"), out.stride(0)
+    if q is not None:
+        ldq = _codes(q, shape, "q").stride(0)
+        _vector(q_scale, T, "q_scale")
+    _check(lib().moe_residual_norm(ctypes.byref(w.c), T, _ptr(x), ax, x.stride(0), _ptr(residual), ar, ldr, _ptr(total),
+                                   lds, _ptr(out), ao, ldo, _ptr(q), ldq, _ptr(q_scale), _stream(stream),
+                                   None if prof is None else ctypes.byref(prof)), "moe_residual_norm")
+
+
+def quant_i8(x, q, q_scale, swiglu: bool = False, stream=None, prof=None):
+    """Rows of x (with swiglu: silu(gate) * up of rows [gate | up]) to codes q and scales q_scale."""
+    T, K = q.shape
+    act = _act(_shaped(x, (T, 2 * K if swiglu else K), "x"), "x")
+    _codes(q, (T, K), "q")
+    _vector(q_scale, T, "q_scale")
+    _check(lib().moe_quant_i8(_ptr(x), act, x.stride(0), T, K, Q8_SWIGLU if swiglu else 0, _ptr(q), q.stride(0),
+                              _ptr(q_scale), _stream(stream), None if prof is None else ctypes.byref(prof)), "moe_quant_i8")
+
+
+class LinearI8:
+    """int8 weights [N, K] (rows at a stride of a multiple of 16 bytes) with a scale per output channel."""
+
+    def __init__(self, w, w_scale, bias=None):
+        self.out_features, self.in_features = w.shape
+        _readable(_codes(w, w.shape, "w"), "w")
+        self.tensors = [w, _vector(w_scale, self.out_features, "w_scale"), _vector(bias, self.out_features, "bias")]
+        self.c = LinearC(self.in_features, self.out_features, w.stride(0), _ptr(w), _ptr(w_scale), _ptr(bias))
+
+    @classmethod
+    def quantize(cls, weight, bias=None, stream=None):
+        """From a bf16 or fp32 weight [N, K]."""
+        import torch
+        N, K = weight.shape
+        w, scale = empty_i8(N, K, weight.device), torch.empty(N, dtype=torch.float32, device=weight.device)
+        quant_i8(weight, w, scale, False, stream)
+        return cls(w, scale, bias)
+
+    def workspace(self, T: int, device="cuda"):
+        import torch
+        return torch.empty(int(lib().moe_linear_i8_workspace_bytes(ctypes.byref(self.c), T)), dtype=torch.uint8, device=device)
+
+
+def linear_i8(w: LinearI8, x, x_scale, y, add=None, ws=None, stream=None, prof=None):
+    """y = (x w^T) * scales + bias + add, for codes x [T, K] with x_scale; add may be y."""
+    T = x.shape[0]
+    _readable(_codes(x, (T, w.in_features), "x"), "x")
+    _vector(x_scale, T, "x_scale")
+    act = _act(_shaped(y, (T, w.out_features), "y"), "y")
+    ldadd = 0
+    if add is not None:
+        ldadd = add.stride(0)
+        if _act(_shaped(add, y.shape, "add"), "add") != act:
+            raise ValueError("add: y's type is needed")
+    _check(lib().moe_linear_i8(ctypes.byref(w.c), T, _ptr(x), x.stride(0), _ptr(x_scale), _ptr(add), ldadd, _ptr(y), act,
+                               y.stride(0), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                               _stream(stream), None if prof is None else ctypes.byref(prof)), "moe_linear_i8")
+
+
+class RouterWeights:
+    """A router [E, H] (fp32) with its score, selection bias, groups and weight rule."""
+
+    def __init__(self, w_router, top_k: int, score: str = "sigmoid", bias=None, n_groups: int = 1, keep_groups: int = 1,
+                 renorm: bool = True, scale: float = 1.0):
+        import torch
+        E, H = w_router.shape
+        if w_router.dtype != torch.float32 or not w_router.is_contiguous():
+            raise ValueError("w_router: contiguous fp32 is needed")
+        self.w_router, self.bias = w_router, _vector(bias, E, "bias")
+        self.hidden, self.n_experts, self.top_k = H, E, top_k
+        self.c = RouterC(H, E, top_k, {"sigmoid": SCORE_SIGMOID, "softmax": SCORE_SOFTMAX}[score], n_groups,
+                         keep_groups, ROUTER_RENORM if renorm else 0, scale, _ptr(w_router), _ptr(bias))
+
+    def workspace(self, T: int, device="cuda"):
+        import torch
+        n = int(lib().moe_route_scored_workspace_bytes(ctypes.byref(self.c), T))
+        return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def route_scored(w: RouterWeights, x, r: Routing, ws, stream=None, prof=None):
+    """Routes the rows of x [T, H] into r (see moe_route_scored)."""
+    T = x.shape[0]
+    act = _act(_shaped(x, (T, w.hidden), "x"), "x")
+    if r.topk_idx.shape != (T, w.top_k) or r.offsets.shape[0] != w.n_experts + 1:
+        raise ValueError("routing buffers of another shape")
+    _check(lib().moe_route_scored(ctypes.byref(w.c), _ptr(x), act, x.stride(0), T, _ptr(r.topk_idx), _ptr(r.topk_w),
+                                  _ptr(r.offsets), _ptr(r.perm), _ptr(r.inv), _ptr(ws), ws.numel() * ws.element_size(),
+                                  _stream(stream), None if prof is None else ctypes.byref(prof)), "moe_route_scored")

@@ -360,6 +360,101 @@ int moe_expert_cache_map(moe_expert_cache *c, int layer_id, const moe_layer *hos
 int moe_expert_cache_prefetch(moe_expert_cache *c, int layer_id, const moe_layer *host_layer,
                               const int32_t *experts_dev, int n, void *stream);
 
+/* ------------------------------------------------------------ scored routing
+ * moe_route_scored: the router with a choice of score, a bias that only the
+ * selection sees, groups of experts, and optional renormalisation:
+ *   l[t,e] = sum_h x[t,h]*W_r[e,h]
+ *   p[t,e] = 1/(1+exp(-l))  (MOE_SCORE_SIGMOID)  or  exp(l) / sum_e' exp(l)  (MOE_SCORE_SOFTMAX)
+ *   c[t,e] = p[t,e] + bias[e]       (bias fp32 [E], device, or NULL)
+ *   group g holds experts g*E/n_groups .. ; its score is the sum of its two
+ *     largest c (its one c if it holds one expert); the keep_groups groups of
+ *     the largest score stay (ties to the lower group), in the others c = -inf
+ *   topk_idx[t,0..k) = the k largest c[t,:], descending, ties to the lower e
+ *   topk_w[t,j] = p_j * scale, with MOE_ROUTER_RENORM divided by sum_j' p_j'
+ *   offsets, perm, inv: as moe_route
+ * The selection is that of fp64 scores: no expert is chosen on a rounding of
+ * fewer bits.  Where c = -inf (a bias of -inf, a group not kept, a NaN score,
+ * which counts as p = 0 and c = -inf) an expert is chosen only if fewer than k
+ * others are left, and then has weight 0; a token with nothing left gets k
+ * weights of 0.  (A logit of +inf has sigmoid 1, and all of the softmax,
+ * shared evenly among several.)
+ * R->n_experts = E <= 1024, top_k = k <= min(64, keep_groups * E / n_groups),
+ * n_groups divides E, hidden H a multiple of 8.  x: [T] rows of H elements of
+ * type act, ldx elements apart; x, w_router ([E][H] fp32) and ws 16-byte
+ * aligned, ldx a multiple of 8.  Workspace: moe_route_scored_workspace_bytes()
+ * (0 if R is invalid). */
+enum moe_score { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
+#define MOE_ROUTER_RENORM 1
+typedef struct moe_router {
+    int32_t hidden, n_experts, top_k;
+    int32_t score, n_groups, keep_groups, flags;
+    float scale;
+    const float *w_router, *bias;
+} moe_router;
+int moe_route_scored(const moe_router *R, const void *x, int act, int64_t ldx, int T, int32_t *topk_idx,
+                     float *topk_w, int32_t *offsets, int32_t *perm, int32_t *inv, void *ws, size_t ws_bytes,
+                     void *stream, moe_profile *prof);
+size_t moe_route_scored_workspace_bytes(const moe_router *R, int T);
+
+/* ------------------------------------------------------------ rows in 8 bits
+ * The dense projections around the routed experts (the pages keep the shared
+ * expert and the attention projections in 8 bits) run on int8 rows: codes
+ * q[t][0..K) with one fp32 scale per row, the value being q * scale.
+ *
+ * Quantizing a row v (fp32): amax = max |v|, scale = amax / 127,
+ *   q = rint(v * (127 / amax)) -- each operation rounded to fp32, so |q| <= 127;
+ *   a row with amax < 2^-100 has scale 0 and q = 0; a row that holds an
+ *   infinity or a NaN has scale NaN and q = 0.
+ *
+ * moe_residual_norm: the residual's addition and the root-mean-square norm
+ *   before a layer, in one pass over the rows:
+ *     s = x + residual  (fp32, rounded to the residual's type; s = x without one)
+ *     v = (s * r) * weight,  r = fp32(1 / sqrt(mean_h s^2 + eps)), the mean in fp64
+ *   sum  (NULL, or the residual's type, may be the residual itself): s
+ *   out  (NULL, or act_out): v rounded;  q, q_scale (both or neither): v as int8
+ *   At least one of out and q.  Every row has its own stride (ld*, in
+ *   elements); element-aligned pointers and strides run, 16-byte aligned rows
+ *   of H % 8 == 0 run fastest.  1 <= hidden <= 65536.
+ * moe_quant_i8: rows of x to int8.  With MOE_Q8_SWIGLU a row of x is [gate K |
+ *   up K] and v = silu(gate) * up, silu(a) = a / (1 + exp(-a)) in fp32.
+ *   1 <= K <= 65536.  Weights are quantized by the same call, a row per output
+ *   channel.
+ * Neither writes outside a row's own columns.  Outputs must not overlap inputs
+ * other than sum on residual. */
+typedef struct moe_norm {
+    int32_t hidden;
+    float eps;
+    const float *weight; /* device fp32 [hidden] */
+} moe_norm;
+int moe_residual_norm(const moe_norm *N, int T, const void *x, int act_x, int64_t ldx, const void *residual,
+                      int act_res, int64_t ldres, void *sum, int64_t ldsum, void *out, int act_out, int64_t ldout,
+                      int8_t *q, int64_t ldq, float *q_scale, void *stream, moe_profile *prof);
+#define MOE_Q8_SWIGLU 1
+int moe_quant_i8(const void *x, int act, int64_t ldx, int T, int K, int flags, int8_t *q, int64_t ldq, float *q_scale,
+                 void *stream, moe_profile *prof);
+
+/* moe_linear_i8: y[t,n] = (sum_k x[t,k]*w[n,k]) * (x_scale[t]*w_scale[n]) + bias[n] + add[t,n]
+ *   The integer sum is exact (int32; K <= 131071); the rest is fp32 in the
+ *   order shown, y rounded once to act_y.  bias: fp32 [N] or NULL.  add: NULL,
+ *   or rows of type act_y, which may be y itself (the shared expert's output
+ *   joins the routed experts' y this way).
+ *   x: int8 codes, rows ldx bytes apart; w: int8 [N] rows ldw bytes apart.  Both
+ *   16-byte aligned with ldx, ldw multiples of 16; bytes K .. round_up(K, 16) of
+ *   a row are read and may hold anything.  y, add: element-aligned, strides in
+ *   elements.
+ *   Workspace: moe_linear_i8_workspace_bytes() (may be 0, then ws may be NULL;
+ *   it never needs clearing); ws 16-byte aligned. */
+typedef struct moe_linear {
+    int32_t in_features, out_features; /* K, N */
+    int64_t ldw;
+    const int8_t *w;
+    const float *w_scale, *bias;
+} moe_linear;
+int moe_linear_i8(const moe_linear *W, int T, const int8_t *x, int64_t ldx, const float *x_scale, const void *add,
+                  int64_t ldadd, void *y, int act_y, int64_t ldy, void *ws, size_t ws_bytes, void *stream,
+                  moe_profile *prof);
+size_t moe_linear_i8_workspace_bytes(const moe_linear *W, int T);
+
 /* ------------------------------------------------------------ pack / unpack
  * q2_pack (host): quantize a row-major fp32 matrix w_host [rows][K] into
  * out_host (q2_packed_bytes(fmt, rows, K) bytes).  fmt: CB2 (needs
