@@ -75,16 +75,25 @@ int check_scored(const moe_router *R)
     return MOE_OK;
 }
 
+// Workspace of a call (p.x_bf16 and p.softmax decide the router)
 size_t scored_ws(ScoredPass &p, char *base)
 {
+    const bool split = scored_split(p.T, p.softmax, p.x_bf16);
     size_t off = 0;
-    p.logits = (double *)base;
-    off = align_up(off + scored_logit_bytes(p.T, p.E));
+    auto take = [&](size_t bytes) {
+        char *at = base + off;
+        off = align_up(off + bytes);
+        return (void *)at;
+    };
+    p.logits = take(scored_logit_bytes(p.T, p.H, p.E, split));
+    if (split) {
+        p.wsplit = take(scored_split_bytes(p.H, p.E));
+        p.wnorm = (float *)take((size_t)p.E * sizeof(float));
+        p.xnorm = (float *)take((size_t)scored_split_parts(p.T, p.H, p.E) * p.T * sizeof(float));
+    }
     if (p.T > SCORED_SMALL_T) {
-        p.rank = (int32_t *)(base + off);
-        off = align_up(off + (size_t)p.T * p.k * sizeof(int32_t));
-        p.tile_counts = (int32_t *)(base + off);
-        off = align_up(off + (size_t)((p.T + 63) / 64) * p.E * sizeof(int32_t));
+        p.rank = (int32_t *)take((size_t)p.T * p.k * sizeof(int32_t));
+        p.tile_counts = (int32_t *)take((size_t)(((int64_t)p.T + 63) / 64) * p.E * sizeof(int32_t));
     }
     return off;
 }
@@ -112,8 +121,15 @@ size_t moe_route_scored_workspace_bytes(const moe_router *R, int T)
 {
     if (T < 0 || check_scored(R)) return 0;
     ScoredPass p{};
-    p.T = T; p.E = R->n_experts; p.k = R->top_k;
-    return scored_ws(p, nullptr);
+    p.T = T; p.H = R->hidden; p.E = R->n_experts; p.k = R->top_k;
+    p.softmax = R->score == MOE_SCORE_SOFTMAX;
+    size_t most = 0;
+    for (int bf16 = 0; bf16 < 2; ++bf16) {       // enough for either activation type
+        p.x_bf16 = bf16;
+        const size_t b = scored_ws(p, nullptr);
+        most = b > most ? b : most;
+    }
+    return most;
 }
 
 int moe_route_scored(const moe_router *R, const void *x, int act, int64_t ldx, int T, int32_t *topk_idx,
@@ -144,8 +160,11 @@ int moe_route_scored(const moe_router *R, const void *x, int act, int64_t ldx, i
     const hipStream_t s = (hipStream_t)stream;
     Launcher run{prof, s};
     auto plain = [](auto f) { return [f] { f(); return hipGetLastError(); }; };
-    if ((rc = run("scored_logits", plain([&] { launch_scored_logits(p, s); })))) return rc;
-    if ((rc = run("scored_topk", plain([&] { launch_scored_topk(p, s); })))) return rc;
+    if (scored_split(T, p.softmax, p.x_bf16)) {
+        if ((rc = run("scored_split", [&] { return launch_scored_split(p, s); }))) return rc;
+        if ((rc = run("scored_split_logits", [&] { return launch_scored_split_logits(p, s); }))) return rc;
+    } else if ((rc = run("scored_logits", [&] { return launch_scored_logits(p, s); }))) return rc;
+    if ((rc = run("scored_topk", [&] { return launch_scored_topk(p, s); })) || T == 1) return rc;
     if (T <= SCORED_SMALL_T)
         return run("route_group_small", plain([&] { launch_route_group_small(topk_idx, T, p.E, p.k, offsets, perm, inv, s); }));
     if ((rc = run("route_rank", plain([&] { launch_route_rank(topk_idx, T, p.E, p.k, p.rank, p.tile_counts, s); })))) return rc;

@@ -16,15 +16,26 @@ struct ScoredPass {
     int32_t *topk_idx;
     float *topk_w;
     int32_t *offsets, *perm, *inv;
-    double *logits;                              // workspace: [T][E]
-    int32_t *rank, *tile_counts;                 // workspace of the grouping (T > SCORED_SMALL_T)
+    // workspace
+    void *logits;                                // fp64 or fp32 [parts][T][E]
+    void *wsplit;                                // split router: the bf16 terms of w
+    float *wnorm, *xnorm;                        // split router: |w_e|^2 [E], |x_t|^2 [parts][T]
+    int32_t *rank, *tile_counts;                 // grouping of more than SCORED_SMALL_T tokens
 };
 
 // up to this many tokens one work-group groups the assignments
 constexpr int SCORED_SMALL_T = 64;
 
-size_t scored_logit_bytes(int T, int E);
-void launch_scored_logits(const ScoredPass &p, hipStream_t s);
-void launch_scored_topk(const ScoredPass &p, hipStream_t s);
+// The split router (see scored.hip): more than SCORED_SMALL_T tokens of bf16 with sigmoid scores.
+inline bool scored_split(int T, bool softmax, bool x_bf16) { return T > SCORED_SMALL_T && !softmax && x_bf16; }
+
+size_t scored_logit_bytes(int T, int H, int E, bool split);
+size_t scored_split_bytes(int H, int E);         // of wsplit
+int scored_split_parts(int T, int H, int E);
+
+hipError_t launch_scored_logits(const ScoredPass &p, hipStream_t s);
+hipError_t launch_scored_split(const ScoredPass &p, hipStream_t s);        // w into its terms
+hipError_t launch_scored_split_logits(const ScoredPass &p, hipStream_t s);
+hipError_t launch_scored_topk(const ScoredPass &p, hipStream_t s);         // T == 1: the grouping too
 
 }  // namespace moe
