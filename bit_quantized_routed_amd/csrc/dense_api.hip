@@ -61,8 +61,8 @@ int check_scored(const moe_router *R)
     if (R->hidden < 8 || R->hidden % 8) return set_error(MOE_ERR_INVALID_ARG, "hidden=%d must be a positive multiple of 8", R->hidden);
     if (R->n_experts < 1 || R->n_experts > 1024) return set_error(MOE_ERR_INVALID_ARG, "n_experts=%d outside [1,1024]", R->n_experts);
     if (R->score != MOE_SCORE_SIGMOID && R->score != MOE_SCORE_SOFTMAX) return set_error(MOE_ERR_INVALID_ARG, "score=%d unknown", R->score);
-    if (R->n_groups < 1 || R->n_experts % R->n_groups)
-        return set_error(MOE_ERR_INVALID_ARG, "n_groups=%d does not divide n_experts=%d", R->n_groups, R->n_experts);
+    if (R->n_groups < 1 || R->n_groups > 64 || R->n_experts % R->n_groups)
+        return set_error(MOE_ERR_INVALID_ARG, "n_groups=%d outside [1,64] or not a divisor of n_experts=%d", R->n_groups, R->n_experts);
     if (R->keep_groups < 1 || R->keep_groups > R->n_groups)
         return set_error(MOE_ERR_INVALID_ARG, "keep_groups=%d outside [1,n_groups]", R->keep_groups);
     const int most = R->keep_groups * (R->n_experts / R->n_groups);
@@ -90,6 +90,7 @@ size_t scored_ws(ScoredPass &p, char *base)
         p.wsplit = take(scored_split_bytes(p.H, p.E));
         p.wnorm = (float *)take((size_t)p.E * sizeof(float));
         p.xnorm = (float *)take((size_t)scored_split_parts(p.T, p.H, p.E) * p.T * sizeof(float));
+        p.open = (int32_t *)take(((size_t)p.T + 1) * sizeof(int32_t));
     }
     if (p.T > SCORED_SMALL_T) {
         p.rank = (int32_t *)take((size_t)p.T * p.k * sizeof(int32_t));

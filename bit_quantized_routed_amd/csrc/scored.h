@@ -20,6 +20,7 @@ struct ScoredPass {
     void *logits;                                // fp64 or fp32 [parts][T][E]
     void *wsplit;                                // split router: the bf16 terms of w
     float *wnorm, *xnorm;                        // split router: |w_e|^2 [E], |x_t|^2 [parts][T]
+    int32_t *open;                               // split router: tokens left to fp64, [0] how many, [1 ..]
     int32_t *rank, *tile_counts;                 // grouping of more than SCORED_SMALL_T tokens
 };
 

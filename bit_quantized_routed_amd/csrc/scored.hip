@@ -110,8 +110,8 @@ __global__ __launch_bounds__(256) void scored_logits64(ScoredPass p, int parts)
 // The terms of w: w1 = bf16(w), w2 = bf16(w - w1), w3 = bf16(w - w1 - w2), each
 // difference exact, w1 + w2 + w3 = w (but for bits below the smallest bf16).
 // They are laid out as the logits kernel's LDS images: [expert block][step of
-// 32 of H][term][64 NG rows][4 chunks of 8 at chunk ^ key(row)], zeros past E
-// and H.
+// 32 of H][w3, w2, w1][64 NG rows][4 chunks of 8 at chunk ^ key(row)], zeros past
+// E and H.
 constexpr int BM = 128;                          // tokens of a work-group
 constexpr int STEP = 32, CHUNK = 128;            // of H: a matrix instruction's depth, a short sum's
 
@@ -123,6 +123,7 @@ __device__ __forceinline__ uint32_t bf16_of(float f) { return __builtin_bit_cast
 
 __global__ __launch_bounds__(256) void scored_split_w(ScoredPass p, int rows)
 {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.open = 0;
     __shared__ float part[4];
     const int e = blockIdx.x, blk = e / rows, r = e % rows, tid = threadIdx.x;
     const int steps = split_steps(p.H);
@@ -150,7 +151,7 @@ __global__ __launch_bounds__(256) void scored_split_w(ScoredPass p, int rows)
                 v[2 * i] -= bf16_bits_to_f32(lo);
                 v[2 * i + 1] -= bf16_bits_to_f32(hi);
             }
-            o[(int64_t)term * rows * 4] = u;
+            o[(int64_t)(2 - term) * rows * 4] = u;
         }
     }
 #pragma unroll
@@ -162,17 +163,22 @@ __global__ __launch_bounds__(256) void scored_split_w(ScoredPass p, int rows)
 
 // Logits of 128 tokens x 64 NG experts over one part of H, fp32 [part][T][E],
 // and the tokens' sums of squares [part][T].  2 NG waves of 64 tokens x 64
-// experts.  x and the three terms of a step of 32 go to LDS without passing
-// registers, one step ahead; the smallest term's products are added first, sums
-// run over 128 of H and are then added to the totals, so that a logit has been
-// rounded 12 times in its short sum and H / 128 times after it.  Parts of H are
-// dealt so that an XCD sees few of them: its share of the terms stays in its L2.
+// experts.  x and the terms go to LDS without passing registers, through rings of
+// three steps of x and eight terms: at the start of step s, whose three terms
+// have landed, those of step s - 1 are free, and the three terms after the five
+// that are there or on their way are requested, with x of step s + 2.  The
+// smallest term's products are added first, sums run over 128 of H and are then
+// added to the totals, so that a logit has been rounded 12 times in its short sum
+// and once for each short sum.  Parts of H are dealt so that an XCD sees few of
+// them: its share of the terms stays in its L2.
+constexpr int XRING = 3, TRING = 8;
+
 template <int NG>
 __global__ __launch_bounds__(128 * NG) void scored_split_logits(ScoredPass p, int parts)
 {
-    constexpr int ROWS = 64 * NG, NW = 2 * NG, XB = BM * 64, TERM = ROWS * 64, SLOT = XB + 3 * TERM;
-    constexpr int LX = BM / 16 / NW, LW = 3 * ROWS / 16 / NW;          // loads of a wave in a step
-    extern __shared__ __align__(16) int8_t ring[];
+    constexpr int ROWS = 64 * NG, NW = 2 * NG, XB = BM * 64, TERM = ROWS * 64;
+    constexpr int LX = BM / 16 / NW, LT = ROWS / 16 / NW;              // loads of a wave: x of a step, a term
+    extern __shared__ __align__(16) int8_t ring[];                     // x [XRING][XB], terms [TRING][TERM]
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int fr = lane & 15, fg = lane >> 4;
     const int part = blockIdx.x % parts, t0 = (int)(blockIdx.x / parts) * BM, blk = blockIdx.y;
@@ -188,24 +194,29 @@ __global__ __launch_bounds__(128 * NG) void scored_split_logits(ScoredPass p, in
         xp[i] = (const uint16_t *)p.x + (int64_t)min(t0 + r, p.T - 1) * p.ldx;
         xc[i] = 8 * (lc ^ key(r));
     }
-    const int8_t *wp = (const int8_t *)p.wsplit + ((int64_t)blk * split_steps(p.H) + begin) * 3 * TERM + wave * LW * 1024 + lane * 16;
-    auto fetch = [&](int s) {
-        int8_t *const buf = ring + (s & 1) * SLOT;
+    const int8_t *wp = (const int8_t *)p.wsplit + ((int64_t)blk * split_steps(p.H) + begin) * 3 * TERM + wave * LT * 1024 + lane * 16;
+    // past the end: the last step again, into slots that nobody reads
+    auto fetch_x = [&](int s) {
+        int8_t *const buf = ring + s % XRING * XB;
 #pragma unroll
         for (int i = 0; i < LX; ++i) {
             // past H: the row's last chunk again, the terms are zero there
-            const int h = min((begin + s) * STEP + xc[i], p.H - 8);
+            const int h = min((begin + min(s, steps - 1)) * STEP + xc[i], p.H - 8);
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(xp[i] + h),
                                              (__attribute__((address_space(3))) void *)(buf + (wave * LX + i) * 1024), 16, 0, 0);
         }
+    };
+    auto fetch_term = [&](int u) {               // term u % 3 of step u / 3
+        int8_t *const buf = ring + XRING * XB + u % TRING * TERM;
+        const int8_t *const at = wp + (int64_t)min(u, 3 * steps - 1) * TERM;
 #pragma unroll
-        for (int i = 0; i < LW; ++i)
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(wp + (int64_t)s * 3 * TERM + i * 1024),
-                                             (__attribute__((address_space(3))) void *)(buf + XB + (wave * LW + i) * 1024), 16, 0, 0);
+        for (int i = 0; i < LT; ++i)
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(at + i * 1024),
+                                             (__attribute__((address_space(3))) void *)(buf + (wave * LT + i) * 1024), 16, 0, 0);
     };
     const int wa = wave % NG, wt = wave / NG;
     const int x0 = 64 * wt + fr, w0 = 64 * wa + fr;
-    const int xo = x0 * 64 + 16 * (fg ^ key(x0)), wo = XB + w0 * 64 + 16 * (fg ^ key(w0));  // + 1024 a fragment
+    const int xo = x0 * 64 + 16 * (fg ^ key(x0)), wo = w0 * 64 + 16 * (fg ^ key(w0));       // + 1024 a fragment
     f32x4 total[4][4], acc[4][4];
     float ss[4];
 #pragma unroll
@@ -214,22 +225,31 @@ __global__ __launch_bounds__(128 * NG) void scored_split_logits(ScoredPass p, in
 #pragma unroll
         for (int j = 0; j < 4; ++j) total[i][j] = acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    fetch(0);
+    fetch_x(0);
+#pragma unroll
+    for (int u = 0; u < 3; ++u) fetch_term(u);
+    fetch_term(3);
+    fetch_term(4);
+    fetch_x(1);
     for (int s = 0; s < steps; ++s) {
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0070);      // vmcnt(0) lgkmcnt(0)
+        // vmcnt: the newest two terms and x may be on their way; lgkmcnt(0)
+        __builtin_amdgcn_s_waitcnt((2 * LT + LX) | 0x70);
         __builtin_amdgcn_s_barrier();            // step s has landed for everybody, and step s - 1 is read
         asm volatile("" ::: "memory");
-        if (s + 1 < steps) fetch(s + 1);
-        const int8_t *buf = ring + (s & 1) * SLOT;
+#pragma unroll
+        for (int u = 5; u < 8; ++u) fetch_term(3 * s + u);
+        fetch_x(s + 2);
+        const int8_t *xbuf = ring + s % XRING * XB;
         bf16x8 b[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = *(const bf16x8 *)(buf + xo + 1024 * j);
+        for (int j = 0; j < 4; ++j) b[j] = *(const bf16x8 *)(xbuf + xo + 1024 * j);
 #pragma unroll
-        for (int term = 2; term >= 0; --term) {
+        for (int term = 0; term < 3; ++term) {   // smallest first
+            const int8_t *tbuf = ring + XRING * XB + (3 * s + term) % TRING * TERM;
             bf16x8 a[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = *(const bf16x8 *)(buf + wo + term * TERM + 1024 * i);
+            for (int i = 0; i < 4; ++i) a[i] = *(const bf16x8 *)(tbuf + wo + 1024 * i);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -256,6 +276,7 @@ __global__ __launch_bounds__(128 * NG) void scored_split_logits(ScoredPass p, in
                 }
         }
     }
+    __builtin_amdgcn_s_waitcnt(0x0f70);          // no load may be in flight when the LDS is freed
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         float v = ss[j];
@@ -334,6 +355,18 @@ __device__ __forceinline__ void token_scores(const ScoredPass &p, const double l
     }
 }
 
+// Wave-wide maximum of floats by DPP (see wave_max_f64); no NaN among them.
+__device__ __forceinline__ float wave_max_f32(float v)
+{
+    auto step = [](float a, int b) { return fmaxf(a, __uint_as_float((uint32_t)b)); };
+    v = step(v, __builtin_amdgcn_mov_dpp((int)__float_as_uint(v), 0xB1, 0xF, 0xF, false));
+    v = step(v, __builtin_amdgcn_mov_dpp((int)__float_as_uint(v), 0x4E, 0xF, 0xF, false));
+    v = step(v, __builtin_amdgcn_mov_dpp((int)__float_as_uint(v), 0x141, 0xF, 0xF, false));
+    v = step(v, __builtin_amdgcn_mov_dpp((int)__float_as_uint(v), 0x140, 0xF, 0xF, false));
+    auto row = [&](int l) { return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), l)); };
+    return fmaxf(fmaxf(row(0), row(16)), fmaxf(row(32), row(48)));
+}
+
 // LDS written before is read after, within one wave: its LDS operations run in
 // order, so only the compiler has to keep it.
 __device__ __forceinline__ void wave_sync()
@@ -343,28 +376,69 @@ __device__ __forceinline__ void wave_sync()
     asm volatile("" ::: "memory");
 }
 
-// This wave's LDS: its token's selection values [E] and group scores [groups],
-// of type V.
-template <typename V>
-struct Groups {
-    V *c, *score, *second;                       // second: the second largest c of a group, -inf for groups of one
-};
-
-// Group scores of one token from c, one wave (p.groups > 1).
+// The parts of a token's logits added in part order, the parts' loads in
+// batches of four.  V: the logits' type; -inf past E.
 template <int MAXPL, typename V>
-__device__ __forceinline__ void group_scores(const ScoredPass &p, int lane, const V c[MAXPL], const Groups<V> &g)
+__device__ __forceinline__ void load_logits(const ScoredPass &p, int t, int parts, int lane, V l[MAXPL])
 {
-    const int G = p.groups, size = p.E / G;
+    const V *in = (const V *)p.logits + (int64_t)t * p.E;
+    const int64_t stride = (int64_t)p.T * p.E;
+#pragma unroll
+    for (int i = 0; i < MAXPL; ++i) l[i] = 0;
+    for (int q0 = 0; q0 < parts; q0 += 4) {
+        V v[4][MAXPL];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < MAXPL; ++i) {
+                v[q][i] = 0;
+                if (q0 + q < parts && lane + 64 * i < p.E) v[q][i] = in[(q0 + q) * stride + lane + 64 * i];
+            }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < MAXPL; ++i) l[i] += v[q][i];
+    }
 #pragma unroll
     for (int i = 0; i < MAXPL; ++i)
-        if (lane + 64 * i < p.E) g.c[lane + 64 * i] = c[i];
+        if (lane + 64 * i >= p.E) l[i] = -INFINITY;
+}
+
+// Groups of one token (p.keep < p.groups <= 64), one wave: lane g's group has
+// `score`, the sum of its two largest c, and `second`, the second of them (the
+// only one where groups hold one expert; then score is it too); bit g of
+// `kept` says whether group g is among the keep best (score descending, group
+// ascending).  cs: this wave's LDS, [E].
+template <typename V>
+struct Groups {
+    V score, second;
+    uint64_t kept;
+};
+
+// group of expert e, by a reciprocal: exact for e < 1024
+__device__ __forceinline__ int group_of(int e, float inv_size) { return (int)(((float)e + 0.5f) * inv_size); }
+
+__device__ __forceinline__ float lane_value(float v, int l)
+{
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), l));
+}
+__device__ __forceinline__ double lane_value(double v, int l) { return readlane_f64(v, l); }
+
+template <int MAXPL, typename V>
+__device__ __forceinline__ Groups<V> rank_groups(const ScoredPass &p, int lane, const V c[MAXPL], V *cs)
+{
+    const int G = p.groups, size = p.E / G;
     wave_sync();
+#pragma unroll
+    for (int i = 0; i < MAXPL; ++i)
+        if (lane + 64 * i < p.E) cs[lane + 64 * i] = c[i];
+    wave_sync();
+    Groups<V> g;
+    V a = -INFINITY, b = -INFINITY;              // the two largest
     if (G <= 8) {                                // 8 lanes a group, then their two largest together
-        const int gr = lane >> 3;
-        V a = -INFINITY, b = -INFINITY;
-        if (gr < G)
+        if ((lane >> 3) < G)
             for (int j = lane & 7; j < size; j += 8) {
-                const V v = g.c[gr * size + j];
+                const V v = cs[(lane >> 3) * size + j];
                 b = fmax(b, fmin(a, v));
                 a = fmax(a, v);
             }
@@ -374,123 +448,93 @@ __device__ __forceinline__ void group_scores(const ScoredPass &p, int lane, cons
             b = fmax(fmin(a, oa), fmax(b, ob));
             a = fmax(a, oa);
         }
-        if (gr < G && (lane & 7) == 0) {
-            g.score[gr] = size > 1 ? a + b : a;
-            g.second[gr] = b;
-        }
-    } else {
-        for (int gr = lane; gr < G; gr += 64) {
-            V a = -INFINITY, b = -INFINITY;
-            for (int j = 0; j < size; ++j) {
-                const V v = g.c[gr * size + j];
-                b = fmax(b, fmin(a, v));
-                a = fmax(a, v);
-            }
-            g.score[gr] = size > 1 ? a + b : a;
-            g.second[gr] = b;
+        a = __shfl(a, (lane & 7) * 8, 64);       // group g's to lane g
+        b = __shfl(b, (lane & 7) * 8, 64);
+    } else if (lane < G) {
+        for (int j = 0; j < size; ++j) {
+            const V v = cs[lane * size + j];
+            b = fmax(b, fmin(a, v));
+            a = fmax(a, v);
         }
     }
-    wave_sync();
-}
-
-// whether group g is among the `keep` best
-template <typename V>
-__device__ __forceinline__ bool group_kept(const ScoredPass &p, const V *score, int g)
-{
-    const V mine = score[g];
+    g.score = size > 1 ? a + b : a;
+    g.second = size > 1 ? b : a;
     int r = 0;
-    for (int o = 0; o < p.groups; ++o) r += score[o] > mine || (score[o] == mine && o < g);
-    return r < p.keep;
+    for (int o = 0; o < G; ++o) {
+        const V s = lane_value(g.score, o);
+        r += s > g.score || (s == g.score && o < lane);
+    }
+    g.kept = __ballot(lane < G && r < p.keep);
+    return g;
 }
 
 // k rounds of a wave-wide arg-max over (c descending, expert ascending): lane
-// j < k keeps slot j's expert and value
+// j < k keeps slot j's expert, value and score
 template <int MAXPL>
-__device__ __forceinline__ void select64(const ScoredPass &p, int lane, const double c[MAXPL], int &my_e, double &my_c,
-                                         uint32_t &taken)
+__device__ __forceinline__ void select64(const ScoredPass &p, int lane, const double c[MAXPL], const double pr[MAXPL], int &my_e,
+                                         double &my_c, double &my_p, uint32_t &taken)
 {
     taken = 0;
     my_e = 0;
-    my_c = 0.0;
+    my_c = my_p = 0.0;
     for (int j = 0; j < p.k; ++j) {
-        double bv = -INFINITY;
+        double bv = -INFINITY, bp = 0.0;
         int be = 0x7fffffff;
 #pragma unroll
         for (int i = 0; i < MAXPL; ++i) {
             const int e = lane + 64 * i;
             // e grows with i, so a strict '>' keeps the lowest expert among equals
-            if (e < p.E && !((taken >> i) & 1u) && (be == 0x7fffffff || c[i] > bv)) { bv = c[i]; be = e; }
+            if (e < p.E && !((taken >> i) & 1u) && (be == 0x7fffffff || c[i] > bv)) { bv = c[i]; bp = pr[i]; be = e; }
         }
         const int mine = be;
         wave_argmax(bv, be);
+        const double sel = readlane_f64(bp, be & 63);   // expert be is lane be % 64's
         if (mine == be) taken |= 1u << (be >> 6);
-        if (lane == j) { my_e = be; my_c = bv; }
+        if (lane == j) { my_e = be; my_c = bv; my_p = sel; }
     }
 }
 
-// value i = be / 64 of lane be % 64
-template <int MAXPL>
-__device__ __forceinline__ double value_of(const double v[MAXPL], int be)
-{
-    double r = 0.0;
-#pragma unroll
-    for (int i = 0; i < MAXPL; ++i) {
-        const double s = __shfl(v[i], be & 63, 64);
-        if (i == be >> 6) r = s;
-    }
-    return r;
-}
-
-// the weights of the chosen experts, w the score of lane j's (0 past k and for c = -inf)
-__device__ __forceinline__ void write_token(const ScoredPass &p, int t, int lane, int my_e, double w)
+// Slot `slot` of token t (slot < k in k lanes of the wave) gets expert e, whose
+// score is w (0 in the other lanes and for c = -inf).
+__device__ __forceinline__ void write_token(const ScoredPass &p, int t, int slot, int e, double w)
 {
     if (p.renorm) {
         const double sum = wave_sum_f64(w);
         w = sum > 0.0 ? w / sum : 0.0;
     }
-    if (lane < p.k) {
-        p.topk_idx[(int64_t)t * p.k + lane] = my_e;
-        p.topk_w[(int64_t)t * p.k + lane] = (float)(w * (double)p.scale);
+    if (slot < p.k) {
+        p.topk_idx[(int64_t)t * p.k + slot] = e;
+        p.topk_w[(int64_t)t * p.k + slot] = (float)(w * (double)p.scale);
     }
 }
 
 constexpr int WAVES = 4;                         // tokens of a work-group, a wave each
+constexpr int EXACT_WAVES = 4;                   // waves of a work-group that share a token
 
 // fp64 selection; a single token is grouped here too (the sorted selection:
 // offsets from ballots of the taken flags)
 template <int MAXPL>
 __global__ __launch_bounds__(64 * WAVES) void scored_topk(ScoredPass p, int parts)
 {
-    extern __shared__ double lds[];              // keep < groups: [WAVES][E + 2 groups]
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    extern __shared__ double lds[];              // keep < groups: [WAVES][E]
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int t = blockIdx.x * (blockDim.x >> 6) + wave;
     if (t >= p.T) return;
     double l[MAXPL], pr[MAXPL], c[MAXPL];
-    const double *in = (const double *)p.logits + (int64_t)t * p.E;
-#pragma unroll
-    for (int i = 0; i < MAXPL; ++i) l[i] = lane + 64 * i < p.E ? in[lane + 64 * i] : -INFINITY;
-    for (int q = 1; q < parts; ++q) {
-        in += (int64_t)p.T * p.E;
-#pragma unroll
-        for (int i = 0; i < MAXPL; ++i)
-            if (lane + 64 * i < p.E) l[i] += in[lane + 64 * i];
-    }
+    load_logits<MAXPL, double>(p, t, parts, lane, l);
     token_scores<MAXPL>(p, l, lane, pr, c);
     if (p.keep < p.groups) {
-        double *mine = lds + (size_t)wave * (p.E + 2 * p.groups);
-        const Groups<double> g{mine, mine + p.E, mine + p.E + p.groups};
-        group_scores<MAXPL, double>(p, lane, c, g);
-        const int size = p.E / p.groups;
+        const Groups<double> g = rank_groups<MAXPL, double>(p, lane, c, lds + (size_t)wave * p.E);
+        const float inv = 1.0f / (float)(p.E / p.groups);
 #pragma unroll
         for (int i = 0; i < MAXPL; ++i)
-            if (lane + 64 * i < p.E && !group_kept(p, g.score, (lane + 64 * i) / size)) c[i] = -INFINITY;
+            if (!(g.kept >> group_of(min(lane + 64 * i, p.E - 1), inv) & 1)) c[i] = -INFINITY;
     }
     int my_e;
-    double my_c;
+    double my_c, my_p;
     uint32_t taken;
-    select64<MAXPL>(p, lane, c, my_e, my_c, taken);
-    const double mine = value_of<MAXPL>(pr, my_e);
-    write_token(p, t, lane, my_e, lane < p.k && my_c != -INFINITY ? mine : 0.0);
+    select64<MAXPL>(p, lane, c, pr, my_e, my_c, my_p, taken);
+    write_token(p, t, lane, my_e, lane < p.k && my_c != -INFINITY ? my_p : 0.0);
     if (p.T > 1) return;
     uint64_t mk[MAXPL];
     int below = 0, base = 0;
@@ -509,195 +553,215 @@ __global__ __launch_bounds__(64 * WAVES) void scored_topk(ScoredPass p, int part
 }
 
 // One expert's logit of one token in fp64 by a whole wave, always in the same
-// order: equal rows of w give equal logits.
+// order: equal rows of w give equal logits.  The loads go in batches of four
+// stretches of 512 of H: their latency is the cost.
 __device__ __forceinline__ double exact_logit(const ScoredPass &p, int t, int e, int lane)
 {
     const uint16_t *x = (const uint16_t *)p.x + (int64_t)t * p.ldx;
     const float *w = p.w + (int64_t)e * p.H;
     double s = 0.0;
-    for (int h = 8 * lane; h < p.H; h += 512) {
-        const u32x4 u = *(const u32x4 *)(x + h);
-        const f32x4 a = *(const f32x4 *)(w + h), b = *(const f32x4 *)(w + h + 4);
+    constexpr int B = 4;
+    for (int h0 = 8 * lane; h0 < p.H; h0 += 512 * B) {
+        u32x4 u[B];
+        f32x4 a[B], b[B];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            s = fma((double)bf16_bits_to_f32((u[i >> 1] >> (16 * (i & 1))) & 0xffffu), (double)(i < 4 ? a[i & 3] : b[i & 3]), s);
+        for (int i = 0; i < B; ++i) {
+            const int h = min(h0 + 512 * i, p.H - 8);
+            u[i] = *(const u32x4 *)(x + h);
+            a[i] = *(const f32x4 *)(w + h);
+            b[i] = *(const f32x4 *)(w + h + 4);
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+            if (h0 + 512 * i < p.H) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    s = fma((double)bf16_bits_to_f32((u[i][j >> 1] >> (16 * (j & 1))) & 0xffffu),
+                            (double)(j < 4 ? a[i][j & 3] : b[i][j & 3]), s);
+            }
     }
     return wave_sum_f64(s);
 }
 
-// replaces the logits of the flagged experts (bit i: expert lane + 64 i) by
-// their fp64 values, and with them pr and c
+// replaces the scores and selection values of the flagged experts (bit i:
+// expert lane + 64 i) that are not done by those of their fp64 logits, shared
+// out over the work-group's waves, which all hold the same token and flags.  ex:
+// LDS [E].
 template <int MAXPL>
-__device__ __forceinline__ void refine(const ScoredPass &p, int t, int lane, uint32_t flags, uint32_t &done, double pr[MAXPL],
-                                       double c[MAXPL])
+__device__ __forceinline__ void refine(const ScoredPass &p, int t, int wave, int lane, uint32_t flags, uint32_t &done,
+                                       double pr[MAXPL], double c[MAXPL], double *ex)
 {
+    int n = 0;
+    __syncthreads();                             // ex is read
 #pragma unroll
     for (int i = 0; i < MAXPL; ++i) {
         uint64_t todo = __ballot((flags & ~done) >> i & 1u);
         while (todo) {
             const int o = __ffsll((unsigned long long)todo) - 1;
             todo &= todo - 1;
-            const double l = exact_logit(p, t, o + 64 * i, lane);
-            if (lane == o) {
-                pr[i] = l != l ? 0.0 : sigmoid64(l);
-                c[i] = biased(p, o + 64 * i, l, pr[i]);
-                done |= 1u << i;
+            if (n++ % EXACT_WAVES == wave) {
+                const double l = exact_logit(p, t, o + 64 * i, lane);
+                if (lane == 0) ex[o + 64 * i] = l;
             }
         }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MAXPL; ++i)
+        if ((flags & ~done) >> i & 1u) {
+            const double l = ex[lane + 64 * i];
+            pr[i] = l != l ? 0.0 : sigmoid64(l);
+            c[i] = biased(p, lane + 64 * i, l, pr[i]);
+        }
+    done |= flags;
+}
+
+// A bound on the error of a token's selection values from the split router's
+// logits.  A logit is off by at most d = rounding |x| max |w_e|: 12 roundings in a
+// short sum, of 2^-23 each (a matrix instruction's own sum included), one of
+// 2^-24 for each short sum of a part and for each part after that, all of values
+// that |x| |w| bounds piece by piece (the pieces' bounds add up to at most the
+// whole's).  In practice the random signs keep it some hundred times smaller.  A
+// selection value is off by at most d / 4, the sigmoid's steepest slope, and
+// fp32's roundings.  Infinite where there is no bound: NaN, or overflow near.
+// c: the experts' biases on return.
+template <int MAXPL>
+__device__ __forceinline__ float value_error(const ScoredPass &p, int t, int parts, float rounding, int lane, float c[MAXPL])
+{
+    float wmax = 0.0f, bmax = 0.0f, xn = 0.0f;
+#pragma unroll
+    for (int i = 0; i < MAXPL; ++i) {
+        const int e = min(lane + 64 * i, p.E - 1);
+        const float n = p.wnorm[e];
+        c[i] = p.bias ? p.bias[e] : 0.0f;
+        wmax = n >= 0.0f ? fmaxf(wmax, n) : INFINITY;
+        if (fabsf(c[i]) < INFINITY) bmax = fmaxf(bmax, fabsf(c[i]));
+    }
+    for (int q = 0; q < parts; ++q) xn += p.xnorm[(int64_t)q * p.T + t];
+    wmax = wave_max_f32(wmax);
+    bmax = wave_max_f32(bmax);
+    const float d = rounding * sqrtf(xn) * sqrtf(wmax);
+    return d < 1e-2f ? 0.25f * d + 0x1p-21f * (1.0f + bmax) : INFINITY;
+}
+
+// The tokens that scored_split_topk left open, a work-group each: every wave
+// holds the whole token and goes the same way, the fp64 logits are shared out.
+// Groups around the border are decided on fp64 values first, then every expert
+// that may be among the k largest.
+template <int MAXPL>
+__global__ __launch_bounds__(64 * EXACT_WAVES) void scored_split_exact(ScoredPass p, int parts, float rounding)
+{
+    __shared__ double ex[64 * MAXPL], cs[EXACT_WAVES][64 * MAXPL];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int n = *p.open;
+    for (int at = blockIdx.x; at < n; at += gridDim.x) {
+        const int t = p.open[1 + at];
+        double pr[MAXPL], c[MAXPL];
+        uint32_t done = 0, flags = 0;
+        float l[MAXPL], bias[MAXPL];
+        load_logits<MAXPL, float>(p, t, parts, lane, l);
+        const double eps = (double)value_error<MAXPL>(p, t, parts, rounding, lane, bias);
+#pragma unroll
+        for (int i = 0; i < MAXPL; ++i) {
+            pr[i] = l[i] != l[i] ? 0.0 : sigmoid64((double)l[i]);
+            c[i] = lane + 64 * i < p.E ? biased(p, lane + 64 * i, (double)l[i], pr[i]) : -INFINITY;
+            if (!(eps < INFINITY) && lane + 64 * i < p.E) flags |= 1u << i;
+        }
+        refine<MAXPL>(p, t, wave, lane, flags, done, pr, c, ex);
+        if (p.keep < p.groups) {
+            const float inv = 1.0f / (float)(p.E / p.groups);
+            Groups<double> g = rank_groups<MAXPL, double>(p, lane, c, cs[wave]);
+            const bool in = g.kept >> lane & 1;
+            const double least = -wave_max_f64(in ? -g.score : -INFINITY);
+            const double most = wave_max_f64(!in && lane < p.groups ? g.score : -INFINITY);
+            flags = 0;
+#pragma unroll
+            for (int i = 0; i < MAXPL; ++i) {
+                const int gr = group_of(min(lane + 64 * i, p.E - 1), inv);
+                const double s = __shfl(g.score, gr, 64), b = __shfl(g.second, gr, 64);
+                if (lane + 64 * i < p.E && !(least - most > 4.0 * eps) && s <= most + 4.0 * eps && s >= least - 4.0 * eps &&
+                    c[i] >= b - 2.0 * eps)
+                    flags |= 1u << i;
+            }
+            refine<MAXPL>(p, t, wave, lane, flags, done, pr, c, ex);
+            g = rank_groups<MAXPL, double>(p, lane, c, cs[wave]);
+#pragma unroll
+            for (int i = 0; i < MAXPL; ++i)
+                if (!(g.kept >> group_of(min(lane + 64 * i, p.E - 1), inv) & 1)) {
+                    c[i] = -INFINITY;
+                    done |= 1u << i;
+                }
+        }
+        int my_e;
+        double my_c, my_p;
+        uint32_t taken;
+        select64<MAXPL>(p, lane, c, pr, my_e, my_c, my_p, taken);
+        const double least = readlane_f64(my_c, p.k - 1) - 2.0 * eps;
+        flags = 0;
+#pragma unroll
+        for (int i = 0; i < MAXPL; ++i)
+            if (lane + 64 * i < p.E && c[i] >= least) flags |= 1u << i;
+        refine<MAXPL>(p, t, wave, lane, flags, done, pr, c, ex);
+        select64<MAXPL>(p, lane, c, pr, my_e, my_c, my_p, taken);
+        if (wave == 0) write_token(p, t, lane, my_e, lane < p.k && my_c != -INFINITY ? my_p : 0.0);
     }
 }
 
-// Selection from the split router's logits.  A logit is off by at most d =
-// rounding |x| max |w_e|: 12 roundings in a short sum, of 2^-23 each (a matrix
-// instruction's own sum included), and up to H / 128 + 8 of 2^-24 after it, all of
-// values that |x| |w| bounds piece by piece.  (In practice the sums' random signs
-// keep it some hundred times smaller.)  A selection value is off by at most eps =
-// d / 4, the sigmoid's steepest slope, and fp32's roundings.  Groups whose scores
-// lie within 4 eps of the border between kept and not, and experts within 2 eps
-// of each other down to the first that is not chosen, are decided on fp64 logits.
+// Selection from the split router's logits where their error leaves no doubt:
+// the scores of kept and other groups more than 4 errors apart, and each of the
+// k largest values, and the next one, more than 2 from its predecessor.  Other
+// tokens go on the list of open ones.
 template <int MAXPL>
 __global__ __launch_bounds__(64 * WAVES) void scored_split_topk(ScoredPass p, int parts, float rounding)
 {
-    extern __shared__ double lds[];              // keep < groups: [WAVES][E + 2 groups]
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    extern __shared__ double lds[];              // keep < groups: [WAVES][E] floats
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int t = blockIdx.x * WAVES + wave;
     if (t >= p.T) return;
     float l[MAXPL], c[MAXPL];
-    float wmax = 0.0f, bmax = 0.0f, xn = lane < parts ? p.xnorm[(int64_t)lane * p.T + t] : 0.0f;
-    const float *in = (const float *)p.logits + (int64_t)t * p.E;
+    load_logits<MAXPL, float>(p, t, parts, lane, l);
+    const float eps = value_error<MAXPL>(p, t, parts, rounding, lane, c);
+    bool open = !(eps < INFINITY);
 #pragma unroll
     for (int i = 0; i < MAXPL; ++i) {
-        const int e = lane + 64 * i;
-        l[i] = -INFINITY;
-        c[i] = 0.0f;                             // the bias for now
-        if (e < p.E) {
-            l[i] = in[e];
-            wmax = fmaxf(wmax, p.wnorm[e]);
-            if (p.bias) c[i] = p.bias[e];
-            if (fabsf(c[i]) < INFINITY) bmax = fmaxf(bmax, fabsf(c[i]));
-        }
-    }
-    for (int q = 1; q < parts; ++q) {
-        in += (int64_t)p.T * p.E;
-#pragma unroll
-        for (int i = 0; i < MAXPL; ++i)
-            if (lane + 64 * i < p.E) l[i] += in[lane + 64 * i];
-    }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        wmax = fmaxf(wmax, __shfl_xor(wmax, off, 64));
-        bmax = fmaxf(bmax, __shfl_xor(bmax, off, 64));
-        xn += __shfl_xor(xn, off, 64);
-    }
-    const float d = rounding * sqrtf(xn) * sqrtf(wmax);
-    const bool sure = d < 1e-2f;                 // no overflow near, no NaN; else everything in fp64
-    const float eps = 0.25f * d + 0x1p-21f * (1.0f + bmax);
-#pragma unroll
-    for (int i = 0; i < MAXPL; ++i) {
-        const float v = l[i] == -INFINITY ? c[i] : 1.0f / (1.0f + expf(-l[i])) + c[i];
+        const float v = 1.0f / (1.0f + expf(-l[i])) + c[i];
         c[i] = lane + 64 * i < p.E && v == v ? v : -INFINITY;
     }
-    const int size = p.E / p.groups;
-    const bool limit = p.keep < p.groups;
-    double *mine64 = lds + (size_t)wave * (p.E + 2 * p.groups);
-    float *mine32 = (float *)mine64;
-    const Groups<float> g{mine32, mine32 + p.E, mine32 + p.E + p.groups};
-    bool open = !sure;
-    float in_least = INFINITY, out_most = -INFINITY;      // scores on both sides of the border
-    float cs[MAXPL];
-#pragma unroll
-    for (int i = 0; i < MAXPL; ++i) cs[i] = c[i];
-    if (limit) {
-        group_scores<MAXPL, float>(p, lane, c, g);
-        for (int gr = lane; gr < p.groups; gr += 64) {
-            const float s = g.score[gr];
-            if (group_kept(p, g.score, gr)) in_least = fminf(in_least, s);
-            else out_most = fmaxf(out_most, s);
-        }
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) {
-            in_least = fminf(in_least, __shfl_xor(in_least, off, 64));
-            out_most = fmaxf(out_most, __shfl_xor(out_most, off, 64));
-        }
-        open = open || !(in_least - out_most > 4.0f * eps);
+    if (p.keep < p.groups) {
+        const Groups<float> g = rank_groups<MAXPL, float>(p, lane, c, (float *)lds + (size_t)wave * p.E);
+        const bool in = g.kept >> lane & 1;
+        const float least = -wave_max_f32(in ? -g.score : -INFINITY);
+        const float most = wave_max_f32(!in && lane < p.groups ? g.score : -INFINITY);
+        open = open || !(least - most > 4.0f * eps);
+        const float inv = 1.0f / (float)(p.E / p.groups);
 #pragma unroll
         for (int i = 0; i < MAXPL; ++i)
-            if (lane + 64 * i < p.E && !group_kept(p, g.score, (lane + 64 * i) / size)) cs[i] = -INFINITY;
+            if (!(g.kept >> group_of(min(lane + 64 * i, p.E - 1), inv) & 1)) c[i] = -INFINITY;
     }
-    // the k + 1 largest; lane j keeps slot j
     int my_e = 0;
-    float my_l = -INFINITY, my_c = -INFINITY;
-    if (!open) {
-        uint32_t taken = 0;
-        float last = INFINITY;
-        for (int j = 0; j <= p.k && j < p.E; ++j) {
-            float bv = -INFINITY, bl = -INFINITY;
-            int be = 0x7fffffff;
+    float my_l = 0.0f, last = INFINITY;
+    uint32_t taken = 0;
+    for (int j = 0; j <= p.k && !open; ++j) {
+        float bv = -INFINITY, bl = 0.0f;
+        int be = 0;
 #pragma unroll
-            for (int i = 0; i < MAXPL; ++i) {
-                const int e = lane + 64 * i;
-                if (e < p.E && !((taken >> i) & 1u) && (be == 0x7fffffff || cs[i] > bv)) { bv = cs[i]; be = e; bl = l[i]; }
-            }
-            float m = bv;
-#pragma unroll
-            for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-            // values this close are told apart in fp64; equal ones too
-            if (!(last - m > 2.0f * eps)) { open = true; break; }
-            if (m == -INFINITY) {                // nothing left: the k-th lies above, or it does not and fp64 says which
-                open = j < p.k;
-                break;
-            }
-            last = m;
-            const uint64_t at = __ballot(bv == m);
-            if (__popcll(at) != 1) { open = true; break; }
-            const int o = __ffsll((unsigned long long)at) - 1;
-            const int e = __builtin_amdgcn_readlane(be, o);
-            const float el = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(bl), o));
-            if (lane == o) taken |= 1u << (e >> 6);
-            if (lane == j) { my_e = e; my_l = el; my_c = m; }
-        }
+        for (int i = 0; i < MAXPL; ++i)
+            if (!((taken >> i) & 1u) && c[i] > bv) { bv = c[i]; bl = l[i]; be = i; }
+        const float m = wave_max_f32(bv);
+        open = !(last - m > 2.0f * eps) || (m == -INFINITY && j < p.k);
+        if (m == -INFINITY) break;
+        const int o = __ffsll((unsigned long long)__ballot(bv == m)) - 1;
+        if (lane == o) taken |= 1u << be;
+        const int e = o + 64 * __builtin_amdgcn_readlane(be, o);
+        const float el = lane_value(bl, o);
+        if (lane == j) { my_e = e; my_l = el; }
+        last = m;
     }
-    if (!open) {
-        write_token(p, t, lane, my_e, lane < p.k && my_c != -INFINITY ? sigmoid64((double)my_l) : 0.0);
+    if (open) {
+        if (lane == 0) p.open[1 + atomicAdd(p.open, 1)] = t;
         return;
     }
-    // ---- in doubt: fp64 for the experts that matter
-    double pr[MAXPL], c64[MAXPL];
-    uint32_t done = 0, flags = 0;
-#pragma unroll
-    for (int i = 0; i < MAXPL; ++i) {
-        pr[i] = l[i] != l[i] ? 0.0 : sigmoid64((double)l[i]);
-        c64[i] = (double)c[i];
-        if (lane + 64 * i >= p.E) continue;
-        const int gr = (lane + 64 * i) / size;
-        const bool near = limit && g.score[gr] <= out_most + 4.0f * eps && g.score[gr] >= in_least - 4.0f * eps &&
-                          c[i] >= g.second[gr] - 2.0f * eps;
-        if (!sure || near) flags |= 1u << i;
-    }
-    refine<MAXPL>(p, t, lane, flags, done, pr, c64);
-    if (limit) {
-        wave_sync();                             // the fp32 scores are read
-        const Groups<double> g64{mine64, mine64 + p.E, mine64 + p.E + p.groups};
-        group_scores<MAXPL, double>(p, lane, c64, g64);
-#pragma unroll
-        for (int i = 0; i < MAXPL; ++i)
-            if (lane + 64 * i < p.E && !group_kept(p, g64.score, (lane + 64 * i) / size)) {
-                c64[i] = -INFINITY;
-                done |= 1u << i;
-            }
-    }
-    double slot_c;
-    uint32_t taken;
-    select64<MAXPL>(p, lane, c64, my_e, slot_c, taken);
-    const double least = __shfl(slot_c, p.k - 1, 64) - 2.0 * (double)eps;
-    flags = 0;
-#pragma unroll
-    for (int i = 0; i < MAXPL; ++i)
-        if (lane + 64 * i < p.E && c64[i] >= least) flags |= 1u << i;
-    refine<MAXPL>(p, t, lane, flags, done, pr, c64);
-    select64<MAXPL>(p, lane, c64, my_e, slot_c, taken);
-    const double w = value_of<MAXPL>(pr, my_e);
-    write_token(p, t, lane, my_e, lane < p.k && slot_c != -INFINITY ? w : 0.0);
+    write_token(p, t, lane, my_e, lane < p.k ? sigmoid64((double)my_l) : 0.0);
 }
 
 }  // namespace
@@ -746,7 +810,7 @@ hipError_t launch_scored_split_logits(const ScoredPass &p, hipStream_t s)
 {
     const int ng = expert_waves(p.E), rows = 64 * ng, parts = scored_split_parts(p.T, p.H, p.E);
     const dim3 grid((unsigned)(((int64_t)p.T + BM - 1) / BM * parts), (unsigned)((p.E + rows - 1) / rows));
-    const size_t lds = 2 * (BM * 64 + 3 * rows * 64);
+    const size_t lds = XRING * BM * 64 + TRING * rows * 64;
 #define MOE_SPLIT(n)                                                                              \
     do {                                                                                          \
         static DevSlots slots{};                                                                  \
@@ -767,19 +831,19 @@ hipError_t launch_scored_topk(const ScoredPass &p, hipStream_t s)
     const int parts = split ? scored_split_parts(p.T, p.H, p.E)
                             : p.T <= SCORED_SMALL_T ? route_decode_chunks(p.T, p.H) : parts64(p.T, p.H, p.E);
     const int waves = p.T == 1 ? 1 : WAVES;
-    const size_t lds = p.keep < p.groups ? (size_t)waves * (p.E + 2 * p.groups) * sizeof(double) : 0;
+    const size_t lds = p.keep < p.groups ? (size_t)waves * p.E * sizeof(double) : 0;
     const unsigned grid = (unsigned)(((int64_t)p.T + waves - 1) / waves);
-    // the short sums' 12 roundings and those after them, in units of 2^-23 of the bound
-    const float rounding = 0x1p-23f * (12.0f + 0.5f * ((float)p.H / CHUNK + 8.0f));
+    // 12 roundings of 2^-23 in a short sum, one of 2^-24 for each short sum of a part and for each part
+    const float rounding = 0x1p-23f * (12.0f + 0.5f * ((float)((p.H + CHUNK - 1) / CHUNK / parts + 1) + (float)parts));
+    // open tokens: two work-groups a CU, more tokens in turns
+    const unsigned exact = (unsigned)std::min(p.T, 512);
     // unrolled for the experts each lane holds (E <= 64 * MAXPL)
 #define MOE_TOPK(pl)                                                                              \
     do {                                                                                          \
-        static DevSlots slots[2]{};                                                               \
-        const void *k = split ? (const void *)scored_split_topk<pl> : (const void *)scored_topk<pl>; \
-        const hipError_t e = lds > 65536 ? lds_limit(k, slots[split], lds) : hipSuccess;          \
-        if (e != hipSuccess) return e;                                                            \
-        if (split) scored_split_topk<pl><<<grid, 64 * WAVES, lds, s>>>(p, parts, rounding);       \
-        else scored_topk<pl><<<grid, 64 * waves, lds, s>>>(p, parts);                             \
+        if (split) {                                                                              \
+            scored_split_topk<pl><<<grid, 64 * WAVES, lds, s>>>(p, parts, rounding);              \
+            scored_split_exact<pl><<<exact, 64 * EXACT_WAVES, 0, s>>>(p, parts, rounding);        \
+        } else scored_topk<pl><<<grid, 64 * waves, lds, s>>>(p, parts);                           \
     } while (0)
     if (p.E <= 64) MOE_TOPK(1);
     else if (p.E <= 128) MOE_TOPK(2);

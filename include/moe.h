@@ -379,7 +379,7 @@ int moe_expert_cache_prefetch(moe_expert_cache *c, int layer_id, const moe_layer
  * weights of 0.  (A logit of +inf has sigmoid 1, and all of the softmax,
  * shared evenly among several.)
  * R->n_experts = E <= 1024, top_k = k <= min(64, keep_groups * E / n_groups),
- * n_groups divides E, hidden H a multiple of 8.  x: [T] rows of H elements of
+ * n_groups <= 64 divides E, hidden H a multiple of 8.  x: [T] rows of H elements of
  * type act, ldx elements apart; x, w_router ([E][H] fp32) and ws 16-byte
  * aligned, ldx a multiple of 8.  Workspace: moe_route_scored_workspace_bytes()
  * (0 if R is invalid). */

@@ -29,7 +29,7 @@ def _route(R, x=FAKE, act=1, ldx=256, T=4, out=FAKE, ws=FAKE, ws_bytes=1 << 40):
 
 @pytest.mark.parametrize("kw", [
     dict(hidden=0), dict(hidden=100), dict(n_experts=0), dict(n_experts=1025, n_groups=1, keep_groups=1), dict(score=2),
-    dict(n_groups=0), dict(n_groups=3), dict(keep_groups=0), dict(keep_groups=5), dict(top_k=0), dict(top_k=9),
+    dict(n_groups=0), dict(n_groups=3), dict(n_experts=256, n_groups=128, keep_groups=100), dict(keep_groups=0), dict(keep_groups=5), dict(top_k=0), dict(top_k=9),
     dict(n_experts=128, n_groups=1, keep_groups=1, top_k=65), dict(flags=2), dict(w_router=None),
     dict(w_router=FAKE + 4), dict(bias=FAKE + 2)])
 def test_router_refusals(kw):
