@@ -90,7 +90,7 @@ size_t scored_ws(ScoredPass &p, char *base)
         p.wsplit = take(scored_split_bytes(p.H, p.E));
         p.wnorm = (float *)take((size_t)p.E * sizeof(float));
         p.xnorm = (float *)take((size_t)scored_split_parts(p.T, p.H, p.E) * p.T * sizeof(float));
-        p.open = (int32_t *)take(((size_t)p.T + 1) * sizeof(int32_t));
+        p.open = (int32_t *)take(scored_open_bytes(p.T));
     }
     if (p.T > SCORED_SMALL_T) {
         p.rank = (int32_t *)take((size_t)p.T * p.k * sizeof(int32_t));

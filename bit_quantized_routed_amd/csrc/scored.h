@@ -20,7 +20,7 @@ struct ScoredPass {
     void *logits;                                // fp64 or fp32 [parts][T][E]
     void *wsplit;                                // split router: the bf16 terms of w
     float *wnorm, *xnorm;                        // split router: |w_e|^2 [E], |x_t|^2 [parts][T]
-    int32_t *open;                               // split router: tokens left to fp64, [0] how many, [1 ..]
+    int32_t *open;                               // split router: the tokens left to fp64, how many and, 16 bytes on, which
     int32_t *rank, *tile_counts;                 // grouping of more than SCORED_SMALL_T tokens
 };
 
@@ -32,6 +32,7 @@ inline bool scored_split(int T, bool softmax, bool x_bf16) { return T > SCORED_S
 
 size_t scored_logit_bytes(int T, int H, int E, bool split);
 size_t scored_split_bytes(int H, int E);         // of wsplit
+size_t scored_open_bytes(int T);                 // of open
 int scored_split_parts(int T, int H, int E);
 
 hipError_t launch_scored_logits(const ScoredPass &p, hipStream_t s);

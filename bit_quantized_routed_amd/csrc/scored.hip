@@ -28,6 +28,7 @@ namespace moe {
 namespace {
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // ---------------------------------------------------------------- fp64 logits
 // More than 64 tokens on the fp64 matrix instructions: 64 tokens x 64 experts
@@ -170,7 +171,10 @@ __global__ __launch_bounds__(256) void scored_split_w(ScoredPass p, int rows)
 // smallest term's products are added first, sums run over 128 of H and are then
 // added to the totals, so that a logit has been rounded 12 times in its short sum
 // and once for each short sum.  Parts of H are dealt so that an XCD sees few of
-// them: its share of the terms stays in its L2.
+// them: its share of the terms stays in its L2.  8192 x 7168 x 256: 100 us for 90
+// Gflop of products (a large library product runs at 1.37 Pflop/s here, 66 us);
+// loads alone 50 us, products and LDS reads 75.  Alternating the waves of a SIMD
+// between reading and multiplying, as the int8 linear layer does, took 105 us.
 constexpr int XRING = 3, TRING = 8;
 
 template <int NG>
@@ -261,9 +265,9 @@ __global__ __launch_bounds__(128 * NG) void scored_split_logits(ScoredPass p, in
         for (int j = 0; j < 4; ++j)
             if (j % NG == wa && blk == 0 && (begin + s) * STEP + 8 * fg < p.H) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float v = (float)b[j][q];
-                    ss[j] = fmaf(v, v, ss[j]);
+                for (int q = 0; q < 8; q += 2) {
+                    const bf16x2 v = {b[j][q], b[j][q + 1]};
+                    ss[j] = __builtin_amdgcn_fdot2_f32_bf16(v, v, ss[j], false);
                 }
             }
         if ((s & 3) == 3) {
@@ -511,6 +515,16 @@ __device__ __forceinline__ void write_token(const ScoredPass &p, int t, int slot
 constexpr int WAVES = 4;                         // tokens of a work-group, a wave each
 constexpr int EXACT_WAVES = 4;                   // waves of a work-group that share a token
 
+// A token left to fp64: `slots` experts in order around the top k with their
+// logits, bit j of close where slot j may not be below slot j - 1; 0 slots: the
+// whole token.
+struct OpenToken {
+    int32_t t, slots;
+    uint64_t close;
+    float logit[64];
+    int16_t expert[64];
+};
+
 // fp64 selection; a single token is grouped here too (the sorted selection:
 // offsets from ballots of the taken flags)
 template <int MAXPL>
@@ -553,14 +567,14 @@ __global__ __launch_bounds__(64 * WAVES) void scored_topk(ScoredPass p, int part
 }
 
 // One expert's logit of one token in fp64 by a whole wave, always in the same
-// order: equal rows of w give equal logits.  The loads go in batches of four
+// order: equal rows of w give equal logits.  The loads go in batches of seven
 // stretches of 512 of H: their latency is the cost.
 __device__ __forceinline__ double exact_logit(const ScoredPass &p, int t, int e, int lane)
 {
     const uint16_t *x = (const uint16_t *)p.x + (int64_t)t * p.ldx;
     const float *w = p.w + (int64_t)e * p.H;
     double s = 0.0;
-    constexpr int B = 4;
+    constexpr int B = 7;
     for (int h0 = 8 * lane; h0 < p.H; h0 += 512 * B) {
         u32x4 u[B];
         f32x4 a[B], b[B];
@@ -644,10 +658,12 @@ __device__ __forceinline__ float value_error(const ScoredPass &p, int t, int par
     return d < 1e-2f ? 0.25f * d + 0x1p-21f * (1.0f + bmax) : INFINITY;
 }
 
-// The tokens that scored_split_topk left open, a work-group each: every wave
-// holds the whole token and goes the same way, the fp64 logits are shared out.
-// Groups around the border are decided on fp64 values first, then every expert
-// that may be among the k largest.
+// The tokens that scored_split_topk left open, a work-group each.  Mostly it
+// names the experts around the top k in order, and which of them are too close to
+// their neighbours: those are summed in fp64, shared out over the waves, and
+// ordered again.  Otherwise every wave holds the whole token and goes the same
+// way: groups around the border are decided on fp64 values first, then every
+// expert that may be among the k largest.
 template <int MAXPL>
 __global__ __launch_bounds__(64 * EXACT_WAVES) void scored_split_exact(ScoredPass p, int parts, float rounding)
 {
@@ -655,7 +671,35 @@ __global__ __launch_bounds__(64 * EXACT_WAVES) void scored_split_exact(ScoredPas
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int n = *p.open;
     for (int at = blockIdx.x; at < n; at += gridDim.x) {
-        const int t = p.open[1 + at];
+        const OpenToken &o = ((const OpenToken *)(p.open + 4))[at];
+        const int t = o.t, slots = o.slots;
+        if (slots > 0) {
+            const uint64_t close = o.close;
+            const int e = lane < slots ? o.expert[lane] : 0;
+            double l = lane < slots ? (double)o.logit[lane] : -INFINITY;
+            uint64_t todo = close | close >> 1;
+            for (int i = 0; todo; ++i) {
+                const int j = __ffsll((unsigned long long)todo) - 1;
+                todo &= todo - 1;
+                if (i % EXACT_WAVES != wave) continue;
+                const double v = exact_logit(p, t, __builtin_amdgcn_readlane(e, j), lane);
+                if (lane == 0) ex[j] = v;
+            }
+            __syncthreads();
+            if (wave == 0) {
+                if ((close | close >> 1) >> lane & 1) l = ex[lane];
+                const double pr = sigmoid64(l), c = lane < slots ? biased(p, e, l, pr) : -INFINITY;
+                int slot = lane < slots ? 0 : p.k;
+                for (int j = 0; j < slots; ++j) {
+                    const double v = readlane_f64(c, j);
+                    const int oe = __builtin_amdgcn_readlane(e, j);
+                    slot += v > c || (v == c && oe < e);
+                }
+                write_token(p, t, slot, e, slot < p.k ? pr : 0.0);
+            }
+            __syncthreads();                     // ex is read
+            continue;
+        }
         double pr[MAXPL], c[MAXPL];
         uint32_t done = 0, flags = 0;
         float l[MAXPL], bias[MAXPL];
@@ -738,30 +782,49 @@ __global__ __launch_bounds__(64 * WAVES) void scored_split_topk(ScoredPass p, in
         for (int i = 0; i < MAXPL; ++i)
             if (!(g.kept >> group_of(min(lane + 64 * i, p.E - 1), inv) & 1)) c[i] = -INFINITY;
     }
-    int my_e = 0;
+    // the largest values in order, lane j keeps slot j, down to the first past k
+    // that is certainly below its predecessor; bit j of close: slot j may not be
+    int my_e = 0, n = 0;
     float my_l = 0.0f, last = INFINITY;
+    uint64_t close = 0;
     uint32_t taken = 0;
-    for (int j = 0; j <= p.k && !open; ++j) {
+    bool end = false;                            // found that first one, or nothing is left
+    while (!open && n < 64) {
         float bv = -INFINITY, bl = 0.0f;
         int be = 0;
 #pragma unroll
         for (int i = 0; i < MAXPL; ++i)
             if (!((taken >> i) & 1u) && c[i] > bv) { bv = c[i]; bl = l[i]; be = i; }
         const float m = wave_max_f32(bv);
-        open = !(last - m > 2.0f * eps) || (m == -INFINITY && j < p.k);
-        if (m == -INFINITY) break;
+        const bool near = !(last - m > 2.0f * eps);
+        end = m == -INFINITY || (n >= p.k && !near);
+        if (end) break;
         const int o = __ffsll((unsigned long long)__ballot(bv == m)) - 1;
+        if (near) close |= 1ull << n;
         if (lane == o) taken |= 1u << be;
         const int e = o + 64 * __builtin_amdgcn_readlane(be, o);
         const float el = lane_value(bl, o);
-        if (lane == j) { my_e = e; my_l = el; }
+        if (lane == n) { my_e = e; my_l = el; }
         last = m;
+        ++n;
     }
-    if (open) {
-        if (lane == 0) p.open[1 + atomicAdd(p.open, 1)] = t;
+    open = open || !end || n < p.k;              // groups, no bound, too many close ones, too few experts
+    if (!open && !close) {
+        write_token(p, t, lane, my_e, lane < p.k ? sigmoid64((double)my_l) : 0.0);
         return;
     }
-    write_token(p, t, lane, my_e, lane < p.k ? sigmoid64((double)my_l) : 0.0);
+    int at = 0;
+    if (lane == 0) at = atomicAdd(p.open, 1);
+    OpenToken &o = ((OpenToken *)(p.open + 4))[__builtin_amdgcn_readfirstlane(at)];
+    if (lane == 0) {
+        o.t = t;
+        o.slots = open ? 0 : n;
+        o.close = close;
+    }
+    if (!open && lane < n) {
+        o.expert[lane] = (int16_t)my_e;
+        o.logit[lane] = my_l;
+    }
 }
 
 }  // namespace
@@ -771,6 +834,8 @@ size_t scored_logit_bytes(int T, int H, int E, bool split)
     if (split) return (size_t)scored_split_parts(T, H, E) * T * E * sizeof(float);
     return (size_t)(T <= SCORED_SMALL_T ? route_decode_chunks(T, H) : parts64(T, H, E)) * T * E * sizeof(double);
 }
+
+size_t scored_open_bytes(int T) { return 4 * sizeof(int32_t) + (size_t)T * sizeof(OpenToken); }
 
 size_t scored_split_bytes(int H, int E)
 {
