@@ -398,46 +398,48 @@ class ExpertCache:
 
 
 # ------------------------------------------------------------------ around the experts
-def _act(t, what: str) -> int:
-    """Activation type of a tensor of rows: fp32 or bf16, elements of a row adjacent."""
+# These calls take a few microseconds on the device for a single token, so the
+# checks here are few attribute reads per tensor.
+_ACTS = {}
+
+
+def _acts():
     import torch
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError("%s: rows of adjacent elements are needed, got shape %s, strides %s"
-                         % (what, tuple(t.shape), t.stride()))
-    if t.dtype == torch.float32:
-        return ACT_F32
-    if t.dtype == torch.bfloat16:
-        return ACT_BF16
-    raise ValueError("%s: fp32 or bf16 is needed, got %s" % (what, t.dtype))
+    _ACTS[torch.float32], _ACTS[torch.bfloat16] = ACT_F32, ACT_BF16
+    return _ACTS
+
+
+def _rows(t, T: int, n: int, what: str):
+    """(activation type, row stride) of T rows of n adjacent elements, fp32 or bf16."""
+    act = (_ACTS or _acts()).get(t.dtype)
+    stride = t.stride()
+    if act is None or t.shape != (T, n) or (stride[1] != 1 and n > 1):
+        raise ValueError("%s: %d rows of %d adjacent fp32 or bf16 elements are needed, got %s of shape %s, strides %s"
+                         % (what, T, n, t.dtype, tuple(t.shape), stride))
+    return act, stride[0]
+
+
+def _codes(t, T: int, n: int, what: str) -> int:
+    """Row stride of T rows of n adjacent int8 codes."""
+    stride = t.stride()
+    if t.element_size() != 1 or not t.dtype.is_signed or t.dtype.is_floating_point or t.shape != (T, n) or (stride[1] != 1 and n > 1):
+        raise ValueError("%s: %d rows of %d adjacent int8 codes are needed, got %s of shape %s, strides %s"
+                         % (what, T, n, t.dtype, tuple(t.shape), stride))
+    return stride[0]
 
 
 def _vector(t, n: int, what: str):
-    import torch
-    if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous()):
+    """fp32 values [n], adjacent, or None."""
+    if t is not None and ((_ACTS or _acts()).get(t.dtype) != ACT_F32 or t.shape != (n,) or not t.is_contiguous()):
         raise ValueError("%s: %d contiguous fp32 values are needed" % (what, n))
-    return t
-
-
-def _shaped(t, shape, what: str):
-    if t is not None and t.shape != shape:
-        raise ValueError("%s: shape %s is needed, got %s" % (what, tuple(shape), tuple(t.shape)))
-    return t
-
-
-def _codes(t, shape, what: str):
-    """Rows of int8 codes, elements of a row adjacent."""
-    import torch
-    if t.dtype != torch.int8 or t.shape != shape or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError("%s: int8 rows of shape %s are needed" % (what, tuple(shape)))
     return t
 
 
 def _readable(t, what: str):
     """moe_linear_i8 reads each row up to the next multiple of 16 bytes: the last row must have them."""
     T, K = t.shape
-    if T and t.storage_offset() + (T - 1) * t.stride(0) + (K + 15) // 16 * 16 > t.untyped_storage().nbytes():
+    if K % 16 and T and t.storage_offset() + (T - 1) * t.stride(0) + (K + 15) // 16 * 16 > t.untyped_storage().nbytes():
         raise ValueError("%s: the last row has no room up to a multiple of 16 bytes (see empty_i8)" % what)
-    return t
 
 
 def empty_i8(T: int, K: int, device="cuda"):
@@ -447,45 +449,48 @@ def empty_i8(T: int, K: int, device="cuda"):
 
 
 class NormWeights:
-    """The weight and epsilon of one residual norm."""
+    """The weight (fp32) and epsilon of one residual norm."""
 
     def __init__(self, weight, eps: float = 1e-6):
         self.weight = _vector(weight, weight.shape[0], "weight")
         self.hidden = weight.shape[0]
         self.c = NormC(self.hidden, eps, _ptr(weight))
+        self.ref = ctypes.byref(self.c)
 
 
 def residual_norm(w: NormWeights, x, residual=None, total=None, out=None, q=None, q_scale=None, stream=None, prof=None):
     """s = x + residual (kept in `total`, which may be `residual`), its norm as `out` and / or as codes q with q_scale."""
-    T, H = x.shape
-    shape = (T, w.hidden)
-    ax = _act(_shaped(x, shape, "x"), "x")
-    ar = ao = 0
-    ldr = lds = ldo = ldq = 0
+    T, H = x.shape[0], w.hidden
+    ax, ldx = _rows(x, T, H, "x")
+    ar = ao = ldr = lds = ldo = ldq = 0
+    pr = pt = po = pq = ps = None
     if residual is not None:
-        ar, ldr = _act(_shaped(residual, shape, "residual"), "residual"), residual.stride(0)
+        ar, ldr = _rows(residual, T, H, "residual")
+        pr = residual.data_ptr()
     if total is not None:
-        lds = total.stride(0)
-        if residual is None or _act(_shaped(total, shape, "total"), "total") != ar:
+        at, lds = _rows(total, T, H, "total")
+        if pr is None or at != ar:
             raise ValueError("total: needs a residual, and its type")
+        pt = total.data_ptr()
     if out is not None:
-        ao, ldo = _act(_shaped(out, shape, "out"), "out"), out.stride(0)
+        ao, ldo = _rows(out, T, H, "out")
+        po = out.data_ptr()
     if q is not None:
-        ldq = _codes(q, shape, "q").stride(0)
-        _vector(q_scale, T, "q_scale")
-    _check(lib().moe_residual_norm(ctypes.byref(w.c), T, _ptr(x), ax, x.stride(0), _ptr(residual), ar, ldr, _ptr(total),
-                                   lds, _ptr(out), ao, ldo, _ptr(q), ldq, _ptr(q_scale), _stream(stream),
-                                   None if prof is None else ctypes.byref(prof)), "moe_residual_norm")
+        ldq, pq = _codes(q, T, H, "q"), q.data_ptr()
+        if q_scale is not None:
+            ps = _vector(q_scale, T, "q_scale").data_ptr()
+    _check((_lib or lib()).moe_residual_norm(w.ref, T, x.data_ptr(), ax, ldx, pr, ar, ldr, pt, lds, po, ao, ldo, pq, ldq, ps,
+                                             _stream(stream), None if prof is None else ctypes.byref(prof)),
+           "moe_residual_norm")
 
 
 def quant_i8(x, q, q_scale, swiglu: bool = False, stream=None, prof=None):
     """Rows of x (with swiglu: silu(gate) * up of rows [gate | up]) to codes q and scales q_scale."""
     T, K = q.shape
-    act = _act(_shaped(x, (T, 2 * K if swiglu else K), "x"), "x")
-    _codes(q, (T, K), "q")
-    _vector(q_scale, T, "q_scale")
-    _check(lib().moe_quant_i8(_ptr(x), act, x.stride(0), T, K, Q8_SWIGLU if swiglu else 0, _ptr(q), q.stride(0),
-                              _ptr(q_scale), _stream(stream), None if prof is None else ctypes.byref(prof)), "moe_quant_i8")
+    act, ldx = _rows(x, T, 2 * K if swiglu else K, "x")
+    _check((_lib or lib()).moe_quant_i8(x.data_ptr(), act, ldx, T, K, Q8_SWIGLU if swiglu else 0, q.data_ptr(),
+                                        _codes(q, T, K, "q"), _vector(q_scale, T, "q_scale").data_ptr(), _stream(stream),
+                                        None if prof is None else ctypes.byref(prof)), "moe_quant_i8")
 
 
 class LinearI8:
@@ -493,9 +498,11 @@ class LinearI8:
 
     def __init__(self, w, w_scale, bias=None):
         self.out_features, self.in_features = w.shape
-        _readable(_codes(w, w.shape, "w"), "w")
+        ldw = _codes(w, self.out_features, self.in_features, "w")
+        _readable(w, "w")
         self.tensors = [w, _vector(w_scale, self.out_features, "w_scale"), _vector(bias, self.out_features, "bias")]
-        self.c = LinearC(self.in_features, self.out_features, w.stride(0), _ptr(w), _ptr(w_scale), _ptr(bias))
+        self.c = LinearC(self.in_features, self.out_features, ldw, _ptr(w), _ptr(w_scale), _ptr(bias))
+        self.ref = ctypes.byref(self.c)
 
     @classmethod
     def quantize(cls, weight, bias=None, stream=None):
@@ -507,24 +514,27 @@ class LinearI8:
         return cls(w, scale, bias)
 
     def workspace(self, T: int, device="cuda"):
+        """A workspace for T tokens (empty where none is needed)."""
         import torch
-        return torch.empty(int(lib().moe_linear_i8_workspace_bytes(ctypes.byref(self.c), T)), dtype=torch.uint8, device=device)
+        return torch.empty(int(lib().moe_linear_i8_workspace_bytes(self.ref, T)), dtype=torch.uint8, device=device)
 
 
 def linear_i8(w: LinearI8, x, x_scale, y, add=None, ws=None, stream=None, prof=None):
     """y = (x w^T) * scales + bias + add, for codes x [T, K] with x_scale; add may be y."""
-    T = x.shape[0]
-    _readable(_codes(x, (T, w.in_features), "x"), "x")
-    _vector(x_scale, T, "x_scale")
-    act = _act(_shaped(y, (T, w.out_features), "y"), "y")
-    ldadd = 0
+    T, N = x.shape[0], w.out_features
+    ldx = _codes(x, T, w.in_features, "x")
+    if w.in_features % 16:
+        _readable(x, "x")
+    act, ldy = _rows(y, T, N, "y")
+    pa, lda = None, 0
     if add is not None:
-        ldadd = add.stride(0)
-        if _act(_shaped(add, y.shape, "add"), "add") != act:
+        aa, lda = _rows(add, T, N, "add")
+        if aa != act:
             raise ValueError("add: y's type is needed")
-    _check(lib().moe_linear_i8(ctypes.byref(w.c), T, _ptr(x), x.stride(0), _ptr(x_scale), _ptr(add), ldadd, _ptr(y), act,
-                               y.stride(0), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-                               _stream(stream), None if prof is None else ctypes.byref(prof)), "moe_linear_i8")
+        pa = add.data_ptr()
+    _check((_lib or lib()).moe_linear_i8(w.ref, T, x.data_ptr(), ldx, _vector(x_scale, T, "x_scale").data_ptr(), pa, lda,
+                                         y.data_ptr(), act, ldy, *((None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)),
+                                         _stream(stream), None if prof is None else ctypes.byref(prof)), "moe_linear_i8")
 
 
 class RouterWeights:
@@ -532,27 +542,29 @@ class RouterWeights:
 
     def __init__(self, w_router, top_k: int, score: str = "sigmoid", bias=None, n_groups: int = 1, keep_groups: int = 1,
                  renorm: bool = True, scale: float = 1.0):
-        import torch
         E, H = w_router.shape
-        if w_router.dtype != torch.float32 or not w_router.is_contiguous():
+        if (_ACTS or _acts()).get(w_router.dtype) != ACT_F32 or not w_router.is_contiguous():
             raise ValueError("w_router: contiguous fp32 is needed")
         self.w_router, self.bias = w_router, _vector(bias, E, "bias")
         self.hidden, self.n_experts, self.top_k = H, E, top_k
         self.c = RouterC(H, E, top_k, {"sigmoid": SCORE_SIGMOID, "softmax": SCORE_SOFTMAX}[score], n_groups,
                          keep_groups, ROUTER_RENORM if renorm else 0, scale, _ptr(w_router), _ptr(bias))
+        self.ref = ctypes.byref(self.c)
 
     def workspace(self, T: int, device="cuda"):
+        """A workspace for T tokens of either activation type."""
         import torch
-        n = int(lib().moe_route_scored_workspace_bytes(ctypes.byref(self.c), T))
+        n = int(lib().moe_route_scored_workspace_bytes(self.ref, T))
         return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
 
 def route_scored(w: RouterWeights, x, r: Routing, ws, stream=None, prof=None):
     """Routes the rows of x [T, H] into r (see moe_route_scored)."""
     T = x.shape[0]
-    act = _act(_shaped(x, (T, w.hidden), "x"), "x")
+    act, ldx = _rows(x, T, w.hidden, "x")
     if r.topk_idx.shape != (T, w.top_k) or r.offsets.shape[0] != w.n_experts + 1:
         raise ValueError("routing buffers of another shape")
-    _check(lib().moe_route_scored(ctypes.byref(w.c), _ptr(x), act, x.stride(0), T, _ptr(r.topk_idx), _ptr(r.topk_w),
-                                  _ptr(r.offsets), _ptr(r.perm), _ptr(r.inv), _ptr(ws), ws.numel() * ws.element_size(),
-                                  _stream(stream), None if prof is None else ctypes.byref(prof)), "moe_route_scored")
+    _check((_lib or lib()).moe_route_scored(w.ref, x.data_ptr(), act, ldx, T, r.topk_idx.data_ptr(), r.topk_w.data_ptr(),
+                                            r.offsets.data_ptr(), r.perm.data_ptr(), r.inv.data_ptr(), ws.data_ptr(),
+                                            ws.nbytes, _stream(stream), None if prof is None else ctypes.byref(prof)),
+           "moe_route_scored")
