@@ -92,7 +92,7 @@ size_t scored_ws(ScoredPass &p, char *base)
         p.xnorm = (float *)take((size_t)scored_split_parts(p.T, p.H, p.E) * p.T * sizeof(float));
         p.open = (int32_t *)take(scored_open_bytes(p.T));
     }
-    if (p.T > SCORED_SMALL_T) {
+    if (!scored_group_fits(p.T, p.E)) {
         p.rank = (int32_t *)take((size_t)p.T * p.k * sizeof(int32_t));
         p.tile_counts = (int32_t *)take((size_t)(((int64_t)p.T + 63) / 64) * p.E * sizeof(int32_t));
     }
@@ -166,8 +166,7 @@ int moe_route_scored(const moe_router *R, const void *x, int act, int64_t ldx, i
         if ((rc = run("scored_split_logits", [&] { return launch_scored_split_logits(p, s); }))) return rc;
     } else if ((rc = run("scored_logits", [&] { return launch_scored_logits(p, s); }))) return rc;
     if ((rc = run("scored_topk", [&] { return launch_scored_topk(p, s); })) || T == 1) return rc;
-    if (T <= SCORED_SMALL_T)
-        return run("route_group_small", plain([&] { launch_route_group_small(topk_idx, T, p.E, p.k, offsets, perm, inv, s); }));
+    if (scored_group_fits(T, p.E)) return run("scored_group", [&] { return launch_scored_group(p, s); });
     if ((rc = run("route_rank", plain([&] { launch_route_rank(topk_idx, T, p.E, p.k, p.rank, p.tile_counts, s); })))) return rc;
     if ((rc = run("route_scan", plain([&] { launch_route_scan(T, p.E, p.k, p.tile_counts, offsets, s); })))) return rc;
     return run("route_scatter", plain([&] {

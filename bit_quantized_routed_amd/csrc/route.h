@@ -31,8 +31,4 @@ void launch_route_partial(const void *x, bool xbf16, int64_t ldx, const float *w
 void launch_route_select(const double *part, const float *bias, int T, int H, int E, int k, int32_t *topk_idx,
                          float *topk_w, int32_t *offsets, int32_t *perm, int32_t *inv, hipStream_t s);
 
-// the grouping alone (T <= 64, k <= 64, E <= 1024)
-void launch_route_group_small(const int32_t *topk_idx, int T, int E, int k, int32_t *offsets, int32_t *perm,
-                              int32_t *inv, hipStream_t s);
-
 }  // namespace moe

@@ -597,12 +597,6 @@ __global__ __launch_bounds__(256) void route_group_small(const int32_t *topk_idx
     group_small(sidx, T, E, k, offsets, perm, inv, mask, cnt);
 }
 
-void launch_route_group_small(const int32_t *topk_idx, int T, int E, int k, int32_t *offsets, int32_t *perm,
-                              int32_t *inv, hipStream_t s)
-{
-    route_group_small<<<1, 256, 0, s>>>(topk_idx, T, E, k, offsets, perm, inv);
-}
-
 int route_decode_chunks(int T, int H)
 {
     // enough waves to spread the W_r stream over the chip at small T; the

@@ -21,10 +21,10 @@ struct ScoredPass {
     void *wsplit;                                // split router: the bf16 terms of w
     float *wnorm, *xnorm;                        // split router: |w_e|^2 [E], |x_t|^2 [parts][T]
     int32_t *open;                               // split router: the tokens left to fp64, how many and, 16 bytes on, which
-    int32_t *rank, *tile_counts;                 // grouping of more than SCORED_SMALL_T tokens
+    int32_t *rank, *tile_counts;                 // grouping where scored_group_fits says no
 };
 
-// up to this many tokens one work-group groups the assignments
+// up to this many tokens the logits are the plain router's partial sums
 constexpr int SCORED_SMALL_T = 64;
 
 // The split router (see scored.hip): more than SCORED_SMALL_T tokens of bf16 with sigmoid scores.
@@ -39,5 +39,8 @@ hipError_t launch_scored_logits(const ScoredPass &p, hipStream_t s);
 hipError_t launch_scored_split(const ScoredPass &p, hipStream_t s);        // w into its terms
 hipError_t launch_scored_split_logits(const ScoredPass &p, hipStream_t s);
 hipError_t launch_scored_topk(const ScoredPass &p, hipStream_t s);         // T == 1: the grouping too
+
+bool scored_group_fits(int T, int E);            // whether one work-group can group the assignments
+hipError_t launch_scored_group(const ScoredPass &p, hipStream_t s);
 
 }  // namespace moe

@@ -456,3 +456,70 @@ def test_profile_names():
     M.linear_i8(lin, codes(2, T, K), torch.ones(T, device="cuda"), y, ws=lin.workspace(T), prof=prof)
     torch.cuda.synchronize()
     assert prof.name == b"linear_i8" and prof.n_launches >= 1 and a.elapsed_time(b) > 0
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("T", [5000, 4096, 1400])
+def test_route_few_experts_many_tokens(T):
+    need_gpu()
+    say("route few experts", T)
+    check_route(T, 64, 3, 2, BF16, "sigmoid", None, 1, 1, True)
+    check_route(T, 64, 1, 1, F32, "softmax", None, 1, 1, True)
+
+
+@pytest.mark.parametrize("T", [1, 32, 200])
+def test_moe_block(T):
+    """The block of bit_quantized_routed_amd.block: its routing from its own norm, the routed experts against the
+    oracle, the shared expert from its codes."""
+    import os
+    import sys
+    need_gpu()
+    say("block", T)
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import moe_block as B
+    import synthetic as S
+    from gpu_common import oracle_experts, rel_l2
+    from oracle import moe_ref as R
+    H, I, E = 512, 256, 16
+    block, gate_up, down = B.make(H, I, E)
+    b = B.BlockBuffers(block, T)
+    x, res = rnd(71, T, H).cuda(), rnd(72, T, H, dtype=BF16).cuda()
+    before = res.clone()
+    y = block(x, res, b)
+    torch.cuda.synchronize()
+    assert torch.equal(res, (x + before.float()).bfloat16())
+    n = b.n.float().cpu().numpy()
+    idx, w = plain_route(n, block.router.w_router.cpu().numpy(), 4, "sigmoid", block.router.bias.cpu().numpy(), 4, 2, True, 2.5)
+    assert np.array_equal(b.routing.topk_idx.cpu().numpy(), idx)
+    cfg = dict(hidden=H, inter=I, n_experts=E, top_k=4, fmt_gate_up=S.FMT_CB2, fmt_down=S.FMT_Q2K, sh_inter=0, seed=0)
+    want = R.moe_layer(n, idx, w, oracle_experts(cfg, range(E)), None)
+    d = lambda t: t.double().cpu()                                     # noqa: E731
+    (wu, su, _), (wd, sd, _) = block.gate_up.tensors, block.down.tensors
+    gu = (d(b.q) * d(b.q_scale)[:, None]) @ (d(wu) * d(su)[:, None]).t()
+    # gate and up to fp32 (3 roundings), then silu: the codes as in test_quant_i8 on top
+    assert rel_l2(b.gate_up.cpu(), gu) < 4 * H24
+    check_codes(d(b.gate_up)[:, :I] * torch.sigmoid(d(b.gate_up)[:, :I]) * d(b.gate_up)[:, I:], b.h, b.h_scale, 7.01 * H24)
+    want = want + ((d(b.h) * d(b.h_scale)[:, None]) @ (d(wd) * d(sd)[:, None]).t()).numpy()
+    assert rel_l2(y.cpu(), want) < (1e-4 if T <= 64 else 5e-3)
+
+
+def test_moe_block_example():
+    import os
+    import sys
+    need_gpu()
+    say("block example")
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import moe_block as B
+    # three quantizations to 8 bits (x, h and the weights): about 1% in all, far below 5%
+    assert B.main(["--tokens", "20", "--hidden", "512", "--inter", "256"]) < 0.05
+
+
+def test_moe_block_refusals():
+    import os
+    import sys
+    need_gpu()
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import moe_block as B
+    block, _, _ = B.make(512, 256, 16)
+    with pytest.raises(ValueError):
+        B.MoeBlock(block.norm, block.router, block.layer, block.down, block.gate_up)
