@@ -15,6 +15,7 @@ using namespace moe;
 namespace {
 
 constexpr size_t ALIGN = 256;
+constexpr int MAX_ROWS = 1 << 22;                // rows of a call, up to 1024 threads each in a launch of fewer than 2^32
 size_t align_up(size_t v) { return (v + ALIGN - 1) / ALIGN * ALIGN; }
 
 int hip_fail(hipError_t e, const char *what) { return set_error(MOE_ERR_HIP, "%s: %s", what, hipGetErrorString(e)); }
@@ -144,6 +145,7 @@ int moe_route_scored(const moe_router *R, const void *x, int act, int64_t ldx, i
     if (prof) prof->n_launches = 0;
     if (T == 0) return MOE_OK;
     if ((int64_t)T * R->top_k > (1 << 30)) return set_error(MOE_ERR_INVALID_ARG, "T*k too large");
+    if (T >= MAX_ROWS) return set_error(MOE_ERR_UNSUPPORTED, "T=%d: more rows than one call takes", T);
     if ((rc = check_rows("x", x, ldx, T, R->hidden, act_size(act)))) return rc;
     if (!topk_idx || !topk_w || !offsets || !perm || !inv) return set_error(MOE_ERR_INVALID_ARG, "NULL tensor argument");
     if (!ws) return set_error(MOE_ERR_INVALID_ARG, "workspace is NULL");
@@ -192,6 +194,7 @@ int moe_residual_norm(const moe_norm *N, int T, const void *x, int act_x, int64_
     if (!out && !q) return set_error(MOE_ERR_INVALID_ARG, "neither out nor q is given");
     if (!q != !q_scale) return set_error(MOE_ERR_INVALID_ARG, "q and q_scale come together");
     const int H = N->hidden;
+    if (T >= MAX_ROWS) return set_error(MOE_ERR_UNSUPPORTED, "T=%d: more rows than one call takes", T);
     if ((rc = check_rows("x", x, ldx, T, H, act_size(act_x)))) return rc;
     if (residual && (rc = check_rows("residual", residual, ldres, T, H, act_size(act_res)))) return rc;
     if (sum && (rc = check_rows("sum", sum, ldsum, T, H, act_size(act_res)))) return rc;
@@ -221,6 +224,7 @@ int moe_quant_i8(const void *x, int act, int64_t ldx, int T, int K, int flags, i
     if (prof) prof->n_launches = 0;
     if (T == 0) return MOE_OK;
     const bool swiglu = (flags & MOE_Q8_SWIGLU) != 0;
+    if (T >= MAX_ROWS) return set_error(MOE_ERR_UNSUPPORTED, "T=%d: more rows than one call takes", T);
     if ((rc = check_rows("x", x, ldx, T, swiglu ? 2 * K : K, act_size(act)))) return rc;
     if ((rc = check_rows("q", q, ldq, T, K, 1))) return rc;
     if (!q_scale || (uintptr_t)q_scale % 4) return set_error(MOE_ERR_INVALID_ARG, "q_scale is NULL or not 4-byte aligned");
@@ -254,7 +258,8 @@ int moe_linear_i8(const moe_linear *W, int T, const int8_t *x, int64_t ldx, cons
     if (!x_scale || (uintptr_t)x_scale % 4) return set_error(MOE_ERR_INVALID_ARG, "x_scale is NULL or not 4-byte aligned");
     if ((rc = check_rows("y", y, ldy, T, N, act_size(act_y)))) return rc;
     if (add && (rc = check_rows("add", add, ldadd, T, N, act_size(act_y)))) return rc;
-    if (((int64_t)T + 15) / 16 * (((int64_t)N + 15) / 16) >= ((int64_t)1 << 31))
+    // a launch holds fewer than 2^32 threads: tiles of at least 32 x 64 with 256 threads, 16 channels with 1024
+    if (((int64_t)T + 31) / 32 * (((int64_t)N + 63) / 64) >= ((int64_t)1 << 24) || N >= 1 << 26)
         return set_error(MOE_ERR_UNSUPPORTED, "T=%d x out_features=%d: too many tiles for one call", T, N);
     const size_t need = linear_ws_bytes(T, N, K);
     if (need && !ws) return set_error(MOE_ERR_INVALID_ARG, "workspace is NULL");

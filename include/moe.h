@@ -373,12 +373,15 @@ int moe_expert_cache_prefetch(moe_expert_cache *c, int layer_id, const moe_layer
  *   topk_w[t,j] = p_j * scale, with MOE_ROUTER_RENORM divided by sum_j' p_j'
  *   offsets, perm, inv: as moe_route
  * The selection is that of fp64 scores: no expert is chosen on a rounding of
- * fewer bits.  Where c = -inf (a bias of -inf, a group not kept, a NaN score,
+ * fewer bits.  The weights are those of fp64 logits, or, for more than 64 bf16
+ * tokens with sigmoid scores, of logits summed in fp32 pieces (within 2^-20 |x|
+ * |w_e| of exact, in practice about 1e-7 of a logit's spread): a token's experts
+ * do not depend on the batch it comes in, its weights only to that.  Where c = -inf (a bias of -inf, a group not kept, a NaN score,
  * which counts as p = 0 and c = -inf) an expert is chosen only if fewer than k
  * others are left, and then has weight 0; a token with nothing left gets k
  * weights of 0.  (A logit of +inf has sigmoid 1, and all of the softmax,
  * shared evenly among several.)
- * R->n_experts = E <= 1024, top_k = k <= min(64, keep_groups * E / n_groups),
+ * T < 2^22 (MOE_ERR_UNSUPPORTED otherwise).  R->n_experts = E <= 1024, top_k = k <= min(64, keep_groups * E / n_groups),
  * n_groups <= 64 divides E, hidden H a multiple of 8.  x: [T] rows of H elements of
  * type act, ldx elements apart; x, w_router ([E][H] fp32) and ws 16-byte
  * aligned, ldx a multiple of 8.  Workspace: moe_route_scored_workspace_bytes()
@@ -419,6 +422,7 @@ size_t moe_route_scored_workspace_bytes(const moe_router *R, int T);
  *   up K] and v = silu(gate) * up, silu(a) = a / (1 + exp(-a)) in fp32.
  *   1 <= K <= 65536.  Weights are quantized by the same call, a row per output
  *   channel.
+ * T < 2^22 for both (MOE_ERR_UNSUPPORTED otherwise: split the rows).
  * Neither writes outside a row's own columns.  Outputs must not overlap inputs
  * other than sum on residual. */
 typedef struct moe_norm {

@@ -44,6 +44,7 @@ def test_route_scored_call_refusals():
                dict(ws=None), dict(ws=FAKE + 8), dict(T=1 << 30)):
         assert _route(R, **kw) == -1, kw
     assert _route(R, ws_bytes=64) == -3
+    assert _route(R, T=1 << 22) == -2
     assert _route(R, T=0, x=None, out=None, ws=None) == 0
     a, b = (M.lib().moe_route_scored_workspace_bytes(ctypes.byref(R), T) for T in (4, 4000))
     assert 0 < a < b
@@ -66,6 +67,7 @@ def test_norm_refusals():
                dict(lds=10), dict(ldo=63), dict(ldq=63), dict(res=None), dict(out=None, q=None, qs=None), dict(q=None),
                dict(qs=None), dict(qs=FAKE + 2), dict(ar=0, res=FAKE + 2), dict(ldx=-64), dict(ldx=BIG + 1)):
         assert _norm(**kw) == -1, kw
+    assert _norm(T=1 << 22) == -2
     assert _norm(T=0, x=None, out=None, q=None, qs=None) == 0
 
 
@@ -79,6 +81,7 @@ def test_quant_refusals():
                dict(q=None), dict(ldq=63), dict(qs=None), dict(qs=FAKE + 1)):
         assert _quant(**kw) == -1, kw
         assert _err()
+    assert _quant(T=1 << 22) == -2 and "rows" in _err()
     assert _quant(T=0, x=None, q=None, qs=None) == 0
 
 
@@ -102,6 +105,7 @@ def test_linear_refusals():
                dict(ws=FAKE + 8)):
         assert _linear(**kw) == -1, kw
     assert _linear(M.LinearC(64, 2 ** 31 - 1, 64, FAKE, FAKE, None), T=2 ** 31 - 1, ldy=2 ** 31) == -2
+    assert _linear(M.LinearC(64, 1 << 26, 64, FAKE, FAKE, None), T=1, ldy=1 << 26) == -2
     assert _linear(T=0, x=None, xs=None, y=None, ws=None) == 0
 
 

@@ -231,6 +231,33 @@ def test_linear_i8(T, N, K, yt, bias, add, pad):
             assert torch.all(y._base[:, N:] == 77)
 
 
+@pytest.mark.parametrize("T,N,K,yt,bias,add", [
+    (4000, 4000, 1, F32, False, False), (4000, 4000, 100, BF16, True, False), (4000, 4000, 128, F32, False, True),
+    (4000, 4000, 130, BF16, False, True), (4000, 4000, 256, BF16, True, True), (3850, 4091, 300, F32, True, False),
+    (4096, 4096, 384, BF16, False, False), (4000, 4001, 513, BF16, True, True), (4096, 4096, 1024, F32, False, False),
+    (2048, 7168, 1400, BF16, False, False), (8192, 4096, 640, BF16, False, False)])
+def test_linear_large(T, N, K, yt, bias, add):
+    """Sizes of the largest tiles, with no, one and several whole steps of K and with ragged ends; the reference is
+    computed in fp64 on the device."""
+    need_gpu()
+    say("linear large", T, N, K, yt, bias, add)
+    x, w = codes(91, T, K), codes(92, N, K)
+    g = torch.Generator(device="cuda").manual_seed(93)
+    xs, ws = (torch.rand(n, generator=g, device="cuda") * 0.01 for n in (T, N))
+    b = torch.randn(N, generator=g, device="cuda") if bias else None
+    a = torch.randn((T, N), generator=g, device="cuda").to(yt) if add else None
+    lin = M.LinearI8(w, ws, b)
+    y = torch.empty((T, N), dtype=yt, device="cuda")
+    M.linear_i8(lin, x, xs, y, a, lin.workspace(T))
+    p = torch.mm(x.double().contiguous(), w.double().t().contiguous())
+    p *= xs.double()[:, None] * ws.double()[None, :]
+    s = p if b is None else p + b.double()
+    ref = s if a is None else s + a.double()
+    tol = H24 * (3.01 * p.abs() + (0 if b is None else 1.01) * s.abs() + (0 if a is None else 1.01) * ref.abs())
+    tol += (h(yt) * 1.001 * (ref.abs() + tol) if yt != F32 else 0) + 1e-38
+    assert torch.all((y.double() - ref).abs() <= tol)
+
+
 @pytest.mark.parametrize("T,N", [(1, 32), (20, 40), (130, 70), (400, 300)])
 def test_linear_largest_sums(T, N):
     """K = 131071 codes of -128: the sum is 2^14 * 131071, just below 2^31."""
@@ -256,6 +283,45 @@ def test_linear_is_the_same_bits_each_time():
         for y in ys:
             M.linear_i8(lin, x, xs, y, ws=wk)
         assert torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2])
+
+
+def test_rows_far_apart():
+    """Strides that put the last rows past 2^31 and 2^32 bytes."""
+    need_gpu()
+    say("far rows")
+    far = 1_100_000_000 // 16 * 16
+    base = torch.empty(5 * far, dtype=torch.int8, device="cuda")
+    T, N, K, H = 5, 33, 200, 264
+
+    def put(t, ld):
+        v = torch.as_strided(base.view(t.dtype), t.shape, (ld, 1))
+        v.copy_(t)
+        return v
+
+    x, w = codes(81, T, K).contiguous(), codes(82, N, K)
+    xs, ws = (rnd(83, T).abs() * 0.01).cuda(), (rnd(84, N).abs() * 0.01).cuda()
+    lin = M.LinearI8(w, ws)
+    y = torch.empty((T, N), device="cuda")
+    M.linear_i8(lin, put(x, far), xs, y, None, lin.workspace(T))
+    check_linear(x, xs, w, ws, None, None, y)
+    lin = M.LinearI8(put(x, far), xs)              # and as weights
+    M.linear_i8(lin, w, ws, yt := torch.empty((N, T), device="cuda"), None, lin.workspace(N))
+    check_linear(w, ws, x, xs, None, None, yt)
+    rows = rnd(85, T, H, dtype=BF16)
+    q, qs = M.empty_i8(T, H), torch.empty(T, device="cuda")
+    M.quant_i8(put(rows.cuda(), far // 2), q, qs)
+    check_codes(rows.double(), q, qs, 0.0)
+    out = torch.empty((T, H), device="cuda")
+    M.residual_norm(M.NormWeights(torch.ones(H, device="cuda"), 0.0), put(rows.cuda(), far // 2), out=out)
+    d = rows.double()
+    v = d / torch.sqrt((d * d).mean(1, keepdim=True))
+    assert torch.all((out.double().cpu() - v).abs() <= 3.02 * H24 * v.abs())
+    xr = rnd(86, T, 64, dtype=BF16)
+    r = M.RouterWeights(rnd(87, 8, 64, std=0.125).cuda(), 2)
+    a, b = M.Routing(T, 2, 8), M.Routing(T, 2, 8)
+    M.route_scored(r, put(xr.cuda(), far // 2), a, r.workspace(T))
+    M.route_scored(r, xr.cuda(), b, r.workspace(T))
+    assert torch.equal(a.topk_idx, b.topk_idx) and torch.equal(a.topk_w, b.topk_w)
 
 
 # ------------------------------------------------------------------ scored routing
@@ -364,6 +430,23 @@ def test_route_near_ties(T):
         w[e, e] = torch.nextafter(w[e, e], torch.tensor(10.0))
     for groups, keep in ((1, 1), (8, 4)):
         check_route(T, H, E, 8, BF16, "sigmoid", None, groups, keep, True, x=rnd(54, T, H, dtype=BF16), w=w)
+
+
+@pytest.mark.parametrize("T", [80, 2000])
+def test_route_scores_on_the_border(T):
+    """Biases that bring every expert's selection value to within 1e-7 of 1 for one token's scores, so that the order
+    turns on bits that fp32 sums do not have; groups as close."""
+    need_gpu()
+    say("route border", T)
+    H, E = 7168, 64
+    w = rnd(58, E, H, std=H ** -0.5)
+    x = rnd(59, 1, H, dtype=BF16)
+    p = 1 / (1 + np.exp(-(x.double().numpy() @ w.double().numpy().T)))[0]
+    bias = torch.from_numpy((1.0 - p + np.random.default_rng(3).uniform(-1e-7, 1e-7, E)).astype(np.float32))
+    xs = x.repeat(T, 1)
+    xs[1::2] = rnd(60, T // 2, H, dtype=BF16)
+    for groups, keep in ((1, 1), (8, 4)):
+        check_route(T, H, E, 8, BF16, "sigmoid", bias, groups, keep, True, x=xs, w=w)
 
 
 @pytest.mark.parametrize("T", [1, 5, 300])
