@@ -108,6 +108,49 @@ __device__ __forceinline__ void finish(const LinearPass &p, int t, int n, const 
     }
 }
 
+// The same for 16 tokens x 16 FA channels of a wave whose rows of y (or add) are
+// not aligned for wide accesses: through LDS (buf: this wave's, 16 (16 FA + 1)
+// floats), so that the lanes of a store hold neighbouring channels of a token.
+// acc: the lane's 4 FA channels, from 4 FA fg on, of token fr.  4118 x 2211 x
+// 968: 34 us, and 67 with each lane storing its own channels.
+template <int FA>
+__device__ __forceinline__ void finish_odd(const LinearPass &p, int t0, int n0, int fr, int fg, const Channels<4 * FA> &c,
+                                           const int acc[4 * FA], float *buf)
+{
+    constexpr int W = 16 * FA, LD = W + 1;
+    const float xs = p.x_scale[min(t0 + fr, p.T - 1)];
+#pragma unroll
+    for (int i = 0; i < 4 * FA; ++i) {
+        float v = (float)acc[i] * (xs * c.scale[i]);
+        if (p.bias) v += c.bias[i];
+        buf[fr * LD + 4 * FA * fg + i] = v;
+    }
+    asm volatile("" ::: "memory");               // one wave: its LDS operations run in order
+    const int lane = 16 * fg + fr, ch = lane % W, n = n0 + ch;
+#pragma unroll 1                                 // small: the callers' loops over fragments have to unroll
+    for (int i = 0; i < 16; i += 64 / W) {
+        const int r = i + lane / W, t = t0 + r;
+        if (t < p.T && n < p.N) {
+            float v = buf[r * LD + ch];
+            const int64_t at = (int64_t)t * p.ldadd + n;
+            if (p.add) v += p.y_bf16 ? bf16_bits_to_f32(((const uint16_t *)p.add)[at]) : ((const float *)p.add)[at];
+            const int64_t yt = (int64_t)t * p.ldy + n;
+            if (p.y_bf16) ((uint16_t *)p.y)[yt] = (uint16_t)to_bf16(v);
+            else ((float *)p.y)[yt] = v;
+        }
+    }
+    asm volatile("" ::: "memory");
+}
+
+// whether rows of y and add start on 16 bytes
+__device__ __forceinline__ bool wide_rows(const LinearPass &p)
+{
+    const int size = p.y_bf16 ? 2 : 4;
+    uintptr_t a = (uintptr_t)p.y | (uintptr_t)(p.ldy * size);
+    if (p.add) a |= (uintptr_t)p.add | (uintptr_t)(p.ldadd * size);
+    return a % 16 == 0;
+}
+
 constexpr int BK = 128;                          // bytes of K per step: eight 16-byte chunks of a row
 
 // Order of the work-groups over the tiles: work-group b runs on XCD b % 8 (each
@@ -303,6 +346,8 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void linear_tile(LinearPass p, int
     // D: lane (fr, fg) of fragment (i, j) holds rows 4 fg .. 4 fg + 3 (channels) of column fr (token)
     const int n = n0 + wa * 16 * FA + 4 * FA * fg;
     const Channels<4 * FA> chan(p, n);
+    const bool odd = parts == 1 && !wide_rows(p);
+    if (odd) __syncthreads();                    // the LDS is read
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
         int v[4 * FA];
@@ -310,7 +355,8 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void linear_tile(LinearPass p, int
         for (int i = 0; i < FA; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[4 * i + r] = acc[i][j][r];
-        if (parts == 1) finish<4 * FA>(p, t0 + xo[j], n, chan, v);
+        if (odd) finish_odd<FA>(p, t0 + xo[j] - fr, n0 + wa * 16 * FA, fr, fg, chan, v, (float *)lds + wave * 16 * (16 * FA + 1));
+        else if (parts == 1) finish<4 * FA>(p, t0 + xo[j], n, chan, v);
         else store_part<4 * FA>(p, part, t0 + xo[j], n, v);
     }
 }
@@ -450,6 +496,8 @@ __global__ __launch_bounds__(512) void linear_big(LinearPass p)
     }
     const int n = n0 + wa * 64 + 16 * fg;
     const Channels<16> chan(p, n);
+    const bool odd = !wide_rows(p);
+    if (odd) __syncthreads();                    // the LDS is read
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
         int v[16];
@@ -457,7 +505,8 @@ __global__ __launch_bounds__(512) void linear_big(LinearPass p)
         for (int i = 0; i < FA; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[4 * i + r] = acc[i][j][r];
-        finish<16>(p, t0 + x0 + 16 * j, n, chan, v);
+        if (odd) finish_odd<FA>(p, t0 + x0 - fr + 16 * j, n0 + wa * 64, fr, fg, chan, v, (float *)lds + wave * 16 * 65);
+        else finish<16>(p, t0 + x0 + 16 * j, n, chan, v);
     }
 }
 
