@@ -452,9 +452,10 @@ __global__ __launch_bounds__(512) void linear_big(LinearPass p)
         int ux = 0;                              // unit of x of this step; w is in the next
         for (int k = 0; k < steps; ++k) {
             const int8_t *xb = lds + ux * UNIT, *wbuf = lds + wrap(ux + 1) * UNIT;
+            reads(xb, wbuf, 0);
+            __builtin_amdgcn_sched_barrier(0);   // the reads first: requests ahead of them cost 2%
             if (second) { if (k + 2 < steps) fetch(wrap(ux + 4)); }
             else if (k + 1 < steps) fetch(wrap(ux + 3));
-            reads(xb, wbuf, 0);
             sync_waves<VM_ANY, 0>();
             __builtin_amdgcn_s_setprio(1);
             products();

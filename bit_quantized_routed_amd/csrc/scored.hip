@@ -241,24 +241,26 @@ __global__ __launch_bounds__(128 * NG) void scored_split_logits(ScoredPass p, in
         __builtin_amdgcn_s_waitcnt((2 * LT + LX) | 0x70);
         __builtin_amdgcn_s_barrier();            // step s has landed for everybody, and step s - 1 is read
         asm volatile("" ::: "memory");
-#pragma unroll
-        for (int u = 5; u < 8; ++u) fetch_term(3 * s + u);
-        fetch_x(s + 2);
         const int8_t *xbuf = ring + s % XRING * XB;
         bf16x8 b[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) b[j] = *(const bf16x8 *)(xbuf + xo + 1024 * j);
+        bf16x8 a[3][4];
 #pragma unroll
-        for (int term = 0; term < 3; ++term) {   // smallest first
-            const int8_t *tbuf = ring + XRING * XB + (3 * s + term) % TRING * TERM;
-            bf16x8 a[4];
+        for (int term = 0; term < 3; ++term)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = *(const bf16x8 *)(tbuf + wo + 1024 * i);
+            for (int i = 0; i < 4; ++i)
+                a[term][i] = *(const bf16x8 *)(ring + XRING * XB + (3 * s + term) % TRING * TERM + wo + 1024 * i);
+        __builtin_amdgcn_sched_barrier(0);       // the reads first
+#pragma unroll
+        for (int u = 5; u < 8; ++u) fetch_term(3 * s + u);
+        fetch_x(s + 2);
+#pragma unroll
+        for (int term = 0; term < 3; ++term)     // smallest first
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = mfma16x16x32(a[i], b[j], acc[i][j]);
-        }
+                for (int j = 0; j < 4; ++j) acc[i][j] = mfma16x16x32(a[term][i], b[j], acc[i][j]);
         // sums of squares of x, the four fragments shared out over the NG waves
         // that hold the same tokens
 #pragma unroll
