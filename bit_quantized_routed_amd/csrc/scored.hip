@@ -962,8 +962,8 @@ hipError_t launch_scored_topk(const ScoredPass &p, hipStream_t s)
     const unsigned grid = (unsigned)(((int64_t)p.T + waves - 1) / waves);
     // 12 roundings of 2^-23 in a short sum, one of 2^-24 for each short sum of a part and for each part
     const float rounding = 0x1p-23f * (12.0f + 0.5f * ((float)((p.H + CHUNK - 1) / CHUNK / parts + 1) + (float)parts));
-    // open tokens: two work-groups a CU, more tokens in turns
-    const unsigned exact = (unsigned)std::min(p.T, 512);
+    // a work-group for each of so many open tokens (those without one end at once), more in turns
+    const unsigned exact = (unsigned)std::min(p.T, 2048);
     // unrolled for the experts each lane holds (E <= 64 * MAXPL)
 #define MOE_TOPK(pl)                                                                              \
     do {                                                                                          \
