@@ -659,7 +659,7 @@ int moe_route(const moe_layer *L, const void *x, int act, int T, const float *bi
     } while (0)
 
     if (route_fused(L, T)) {
-        MOE_LAUNCH("route_partial", launch_route_partial(x, act == MOE_ACT_BF16, L->hidden, L->w_router, T, H, E, w.logits, s));
+        MOE_LAUNCH("route_partial", launch_route_partial(x, act == MOE_ACT_BF16, L->w_router, T, H, E, w.logits, s));
         MOE_LAUNCH("route_select", launch_route_select(w.logits, bias, T, H, E, k, topk_idx, topk_w, offsets, perm,
                                                        inv, s));
         return MOE_OK;

@@ -356,7 +356,7 @@ __global__ __launch_bounds__(GU_THREADS) void dec1_gateup_kernel(DecPass p)
             // the items first, spread over the whole grid
             if (p.route) {
                 for (int it = item; it < p.E * p.rnc; it += nw)
-                    route_partial_item<1, 1, !XF32>(p.x, H, p.wr, 1, H, p.E, p.rnc, p.rhc, it, lane, p.rpart);
+                    route_partial_item<1, 1, !XF32>(p.x, p.wr, 1, H, p.E, p.rnc, p.rhc, it, lane, p.rpart);
             }
             for (int i = tid; i < H / 8; i += GU_THREADS) {
                 if (XF32) {

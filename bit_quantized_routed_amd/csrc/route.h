@@ -26,7 +26,7 @@ void launch_route_scatter(const int32_t *topk_idx, const int32_t *rank, const in
 // small-T router (T <= 64, k <= 64, E <= 1024): partial logits, then one
 // work-group selects and groups
 int route_decode_chunks(int T, int H);
-void launch_route_partial(const void *x, bool xbf16, int64_t ldx, const float *wr, int T, int H, int E, double *part,
+void launch_route_partial(const void *x, bool xbf16, const float *wr, int T, int H, int E, double *part,
                           hipStream_t s);
 void launch_route_select(const double *part, const float *bias, int T, int H, int E, int k, int32_t *topk_idx,
                          float *topk_w, int32_t *offsets, int32_t *perm, int32_t *inv, hipStream_t s);

@@ -459,13 +459,13 @@ void launch_route_scatter(const int32_t *topk_idx, const int32_t *rank, const in
 namespace moe {
 
 template <int EW, int TB, bool XBF16>
-__global__ __launch_bounds__(256) void route_partial(const void *x, int64_t ldx, const float *wr, int T, int H,
-                                                     int E, int NC, int HC, double *part)
+__global__ __launch_bounds__(256) void route_partial(const void *x, const float *wr, int T, int H, int E, int NC,
+                                                     int HC, double *part)
 {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int item = blockIdx.x * 4 + wave;
     if (item >= (E / EW) * ((T + TB - 1) / TB) * NC) return;
-    route_partial_item<EW, TB, XBF16>(x, ldx, wr, T, H, E, NC, HC, item, lane, part);
+    route_partial_item<EW, TB, XBF16>(x, wr, T, H, E, NC, HC, item, lane, part);
 }
 
 // Exact top-k of one token by rank counting: thread e counts the experts that
@@ -606,8 +606,7 @@ int route_decode_chunks(int T, int H)
     return std::min(4, steps);
 }
 
-void launch_route_partial(const void *x, bool xbf16, int64_t ldx, const float *wr, int T, int H, int E, double *part,
-                          hipStream_t s)
+void launch_route_partial(const void *x, bool xbf16, const float *wr, int T, int H, int E, double *part, hipStream_t s)
 {
     const int NC = route_decode_chunks(T, H);
     const int steps = (H + 255) / 256;
@@ -616,7 +615,7 @@ void launch_route_partial(const void *x, bool xbf16, int64_t ldx, const float *w
     const int TB = T <= 2 ? 1 : 8;
     const int items = (E / EW) * ((T + TB - 1) / TB) * NC;
     const int grid = (items + 3) / 4;
-#define MOE_RP(ew, tb, xb) route_partial<ew, tb, xb><<<grid, 256, 0, s>>>(x, ldx, wr, T, H, E, NC, HC, part)
+#define MOE_RP(ew, tb, xb) route_partial<ew, tb, xb><<<grid, 256, 0, s>>>(x, wr, T, H, E, NC, HC, part)
     if (EW == 4) { if (xbf16) MOE_RP(4, 8, true); else MOE_RP(4, 8, false); }
     else if (TB == 8) { if (xbf16) MOE_RP(1, 8, true); else MOE_RP(1, 8, false); }
     else { if (xbf16) MOE_RP(1, 1, true); else MOE_RP(1, 1, false); }

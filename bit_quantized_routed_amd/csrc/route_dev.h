@@ -10,11 +10,10 @@
 namespace moe {
 
 // One wave's item of the partial logits: EW experts x TB tokens over one H
-// chunk (item < (E / EW) * ceil(T / TB) * NC), written to part[c][t][e].  Rows
-// of x are ldx elements apart.
+// chunk (item < (E / EW) * ceil(T / TB) * NC), written to part[c][t][e].
 template <int EW, int TB, bool XBF16>
-__device__ __forceinline__ void route_partial_item(const void *x, int64_t ldx, const float *wr, int T, int H, int E,
-                                                   int NC, int HC, int item, int lane, double *part)
+__device__ __forceinline__ void route_partial_item(const void *x, const float *wr, int T, int H, int E, int NC, int HC,
+                                                   int item, int lane, double *part)
 {
     (void)E;
     const int n_tg = (T + TB - 1) / TB;
@@ -43,8 +42,8 @@ __device__ __forceinline__ void route_partial_item(const void *x, int64_t ldx, c
 #pragma unroll
                 for (int b = 0; b < TB; ++b)
                     if (b < nt) {
-                        if (XBF16) xb[st][b] = *(const uint2 *)&((const uint16_t *)x)[(int64_t)(t0 + b) * ldx + h];
-                        else xf[st][b] = *(const f32x4 *)&((const float *)x)[(int64_t)(t0 + b) * ldx + h];
+                        if (XBF16) xb[st][b] = *(const uint2 *)&((const uint16_t *)x)[(size_t)(t0 + b) * H + h];
+                        else xf[st][b] = *(const f32x4 *)&((const float *)x)[(size_t)(t0 + b) * H + h];
                     }
             }
         }

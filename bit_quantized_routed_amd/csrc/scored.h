@@ -24,7 +24,7 @@ struct ScoredPass {
     int32_t *rank, *tile_counts;                 // grouping where scored_group_fits says no
 };
 
-// up to this many tokens the logits are the plain router's partial sums
+// up to this many tokens the logits are sums of a wave each
 constexpr int SCORED_SMALL_T = 64;
 
 // The split router (see scored.hip): more than SCORED_SMALL_T tokens of bf16 with sigmoid scores.

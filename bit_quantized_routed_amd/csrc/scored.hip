@@ -17,7 +17,6 @@
 //   Softmax stays in fp64: there every score hangs on the sum over all experts.
 #include "common.h"
 #include "devcache.h"
-#include "route.h"
 #include "route_dev.h"
 #include "scored.h"
 
@@ -31,6 +30,74 @@ typedef double f64x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // ---------------------------------------------------------------- fp64 logits
+// Up to 64 tokens: a wave sums EW experts x TB tokens over one part of H, 8
+// values a lane and step, every load of two steps on its way before the first
+// product; a fixed butterfly adds the lanes.  Partial sums [part][T][E].
+constexpr int PARTS_SMALL = 4;
+
+int parts_small(int H) { return std::min(PARTS_SMALL, (H + 511) / 512); }
+
+template <int EW, int TB, bool XBF16>
+__global__ __launch_bounds__(256) void scored_partial(ScoredPass p, int parts)
+{
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int tgroups = (p.T + TB - 1) / TB, item = blockIdx.x * 4 + wave;
+    if (item >= (p.E + EW - 1) / EW * tgroups * parts) return;
+    const int part = item % parts, t0 = item / parts % tgroups * TB, e0 = item / (parts * tgroups) * EW;
+    const int steps = (p.H + 511) / 512;
+    const int begin = steps * part / parts * 512, end = min(p.H, steps * (part + 1) / parts * 512);
+    double acc[EW][TB];
+#pragma unroll
+    for (int a = 0; a < EW; ++a)
+#pragma unroll
+        for (int b = 0; b < TB; ++b) acc[a][b] = 0.0;
+    constexpr int B = TB == 1 ? 4 : 1;           // steps loaded together
+    for (int h0 = begin + 8 * lane; h0 < end; h0 += 512 * B) {
+        f32x4 w[B][EW][2];
+        u32x4 x[B][TB][XBF16 ? 1 : 2];
+#pragma unroll
+        for (int s = 0; s < B; ++s) {
+            const int h = min(h0 + 512 * s, p.H - 8);
+#pragma unroll
+            for (int a = 0; a < EW; ++a)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) w[s][a][q] = *(const f32x4 *)(p.w + (int64_t)min(e0 + a, p.E - 1) * p.H + h + 4 * q);
+#pragma unroll
+            for (int b = 0; b < TB; ++b) {
+                const int64_t at = (int64_t)min(t0 + b, p.T - 1) * p.ldx + h;
+                if (XBF16) x[s][b][0] = *(const u32x4 *)((const uint16_t *)p.x + at);
+                else {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) x[s][b][q] = *(const u32x4 *)((const float *)p.x + at + 4 * q);
+                }
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < B; ++s)
+            if (h0 + 512 * s < end) {
+#pragma unroll
+                for (int b = 0; b < TB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        double xv;
+                        if (XBF16) xv = (double)bf16_bits_to_f32((x[s][b][0][i >> 1] >> (16 * (i & 1))) & 0xffffu);
+                        else xv = (double)__uint_as_float(x[s][b][i >> 2][i & 3]);
+#pragma unroll
+                        for (int a = 0; a < EW; ++a) acc[a][b] = fma(xv, (double)w[s][a][i >> 2][i & 3], acc[a][b]);
+                    }
+            }
+    }
+#pragma unroll
+    for (int a = 0; a < EW; ++a)
+#pragma unroll
+        for (int b = 0; b < TB; ++b) {
+#pragma unroll
+            for (int off = 32; off > 0; off >>= 1) acc[a][b] += __shfl_xor(acc[a][b], off, 64);
+            if (lane == a * TB + b && t0 + b < p.T && e0 + a < p.E)
+                ((double *)p.logits)[((int64_t)part * p.T + t0 + b) * p.E + e0 + a] = acc[a][b];
+        }
+}
+
 // More than 64 tokens on the fp64 matrix instructions: 64 tokens x 64 experts
 // and one part of H per work-group, partial sums [part][T][E].  Chunks of 32 of
 // H pass through LDS as fp64, the next one's values on their way into
@@ -894,7 +961,7 @@ __global__ __launch_bounds__(1024) void scored_group(const int32_t *topk_idx, in
 size_t scored_logit_bytes(int T, int H, int E, bool split)
 {
     if (split) return (size_t)scored_split_parts(T, H, E) * T * E * sizeof(float);
-    return (size_t)(T <= SCORED_SMALL_T ? route_decode_chunks(T, H) : parts64(T, H, E)) * T * E * sizeof(double);
+    return (size_t)(T <= SCORED_SMALL_T ? parts_small(H) : parts64(T, H, E)) * T * E * sizeof(double);
 }
 
 size_t scored_open_bytes(int T) { return 4 * sizeof(int32_t) + (size_t)T * sizeof(OpenToken); }
@@ -916,7 +983,17 @@ int scored_split_parts(int T, int H, int E)
 hipError_t launch_scored_logits(const ScoredPass &p, hipStream_t s)
 {
     if (p.T <= SCORED_SMALL_T) {
-        launch_route_partial(p.x, p.x_bf16, p.ldx, p.w, p.T, p.H, p.E, (double *)p.logits, s);
+        // one token: a wave per expert; more: eight tokens and two experts a wave share what they load
+        const int parts = parts_small(p.H), tb = p.T == 1 ? 1 : 8, ew = p.T == 1 ? 1 : 2;
+        const int items = (p.E + ew - 1) / ew * ((p.T + tb - 1) / tb) * parts;
+        const unsigned grid = (unsigned)((items + 3) / 4);
+        if (p.T == 1) {
+            if (p.x_bf16) scored_partial<1, 1, true><<<grid, 256, 0, s>>>(p, parts);
+            else scored_partial<1, 1, false><<<grid, 256, 0, s>>>(p, parts);
+        } else {
+            if (p.x_bf16) scored_partial<2, 8, true><<<grid, 256, 0, s>>>(p, parts);
+            else scored_partial<2, 8, false><<<grid, 256, 0, s>>>(p, parts);
+        }
         return hipGetLastError();
     }
     const int parts = parts64(p.T, p.H, p.E);
@@ -956,7 +1033,7 @@ hipError_t launch_scored_topk(const ScoredPass &p, hipStream_t s)
 {
     const bool split = scored_split(p.T, p.softmax, p.x_bf16);
     const int parts = split ? scored_split_parts(p.T, p.H, p.E)
-                            : p.T <= SCORED_SMALL_T ? route_decode_chunks(p.T, p.H) : parts64(p.T, p.H, p.E);
+                            : p.T <= SCORED_SMALL_T ? parts_small(p.H) : parts64(p.T, p.H, p.E);
     const int waves = p.T == 1 ? 1 : WAVES;
     const size_t lds = p.keep < p.groups ? (size_t)waves * p.E * sizeof(double) : 0;
     const unsigned grid = (unsigned)(((int64_t)p.T + waves - 1) / waves);
