@@ -79,7 +79,7 @@ int check_scored(const moe_router *R)
 // Workspace of a call (p.x_bf16 and p.softmax decide the router)
 size_t scored_ws(ScoredPass &p, char *base)
 {
-    const bool split = scored_split(p.T, p.softmax, p.x_bf16);
+    const bool split = scored_split(p.T, p.E, p.softmax, p.x_bf16);
     size_t off = 0;
     auto take = [&](size_t bytes) {
         char *at = base + off;
@@ -163,7 +163,7 @@ int moe_route_scored(const moe_router *R, const void *x, int act, int64_t ldx, i
     const hipStream_t s = (hipStream_t)stream;
     Launcher run{prof, s};
     auto plain = [](auto f) { return [f] { f(); return hipGetLastError(); }; };
-    if (scored_split(T, p.softmax, p.x_bf16)) {
+    if (scored_split(T, p.E, p.softmax, p.x_bf16)) {
         if ((rc = run("scored_split", [&] { return launch_scored_split(p, s); }))) return rc;
         if ((rc = run("scored_split_logits", [&] { return launch_scored_split_logits(p, s); }))) return rc;
     } else if ((rc = run("scored_logits", [&] { return launch_scored_logits(p, s); }))) return rc;

@@ -25,10 +25,17 @@ struct ScoredPass {
 };
 
 // up to this many tokens the logits are sums of a wave each
-constexpr int SCORED_SMALL_T = 64;
+constexpr int SCORED_SMALL_T = 128;
 
-// The split router (see scored.hip): more than SCORED_SMALL_T tokens of bf16 with sigmoid scores.
-inline bool scored_split(int T, bool softmax, bool x_bf16) { return T > SCORED_SMALL_T && !softmax && x_bf16; }
+// The split router (see scored.hip): bf16 tokens with sigmoid scores, and enough
+// of them.  Its launches have a floor (the terms of w, the open tokens) that the
+// fp64 matrix instructions only reach past 640 tokens of 256 experts: H = 7168,
+// T = 333 / 500 / 700 / 1000 / 1400 / 2048 take 64 / 66 / 93 / 94 / 160 / 165 us
+// in fp64 and 83 / 85 / 87 / 89 / 93 / 94 us split.
+inline bool scored_split(int T, int E, bool softmax, bool x_bf16)
+{
+    return T > SCORED_SMALL_T && (int64_t)T * E > 640 * 256 && !softmax && x_bf16;
+}
 
 size_t scored_logit_bytes(int T, int H, int E, bool split);
 size_t scored_split_bytes(int H, int E);         // of wsplit

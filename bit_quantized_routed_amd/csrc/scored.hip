@@ -30,7 +30,7 @@ typedef double f64x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // ---------------------------------------------------------------- fp64 logits
-// Up to 64 tokens: a wave sums EW experts x TB tokens over one part of H, 8
+// Up to 128 tokens: a wave sums EW experts x TB tokens over one part of H, 8
 // values a lane and step, every load of two steps on its way before the first
 // product; a fixed butterfly adds the lanes.  Partial sums [part][T][E].
 constexpr int PARTS_SMALL = 4;
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(256) void scored_partial(ScoredPass p, int parts)
         }
 }
 
-// More than 64 tokens on the fp64 matrix instructions: 64 tokens x 64 experts
+// More tokens on the fp64 matrix instructions: 64 tokens x 64 experts
 // and one part of H per work-group, partial sums [part][T][E].  Chunks of 32 of
 // H pass through LDS as fp64, the next one's values on their way into
 // registers meanwhile; rows of 33 doubles put the 16 lanes of a read on
@@ -448,6 +448,9 @@ __device__ __forceinline__ float wave_max_f32(float v)
     return fmaxf(fmaxf(row(0), row(16)), fmaxf(row(32), row(48)));
 }
 
+__device__ __forceinline__ float wave_max(float v) { return wave_max_f32(v); }
+__device__ __forceinline__ double wave_max(double v) { return wave_max_f64(v); }
+
 // LDS written before is read after, within one wave: its LDS operations run in
 // order, so only the compiler has to keep it.
 __device__ __forceinline__ void wave_sync()
@@ -735,12 +738,80 @@ __device__ __forceinline__ float value_error(const ScoredPass &p, int t, int par
     return d < 1e-2f ? 0.25f * d + 0x1p-21f * (1.0f + bmax) : INFINITY;
 }
 
+// The experts around the top k in order, lane j slot j with its expert, value c
+// and companion v (a logit or a score): down to the first past k that is more than
+// 2 eps below its predecessor, at most 64.  Bit j of close: slot j is not.  Returns
+// whether that first one was found (or nothing was left) with at least k slots.
+template <int MAXPL, typename V>
+__device__ __forceinline__ bool order_slots(const ScoredPass &p, int lane, const V c[MAXPL], const V v[MAXPL], V eps, int &my_e,
+                                            V &my_c, V &my_v, int &n, uint64_t &close)
+{
+    uint32_t taken = 0;
+    V last = INFINITY;
+    my_e = 0;
+    my_c = -INFINITY;
+    my_v = 0;
+    n = 0;
+    close = 0;
+    while (n < 64) {
+        V bc = -INFINITY, bv = 0;
+        int bi = 0;
+#pragma unroll
+        for (int i = 0; i < MAXPL; ++i)
+            if (!((taken >> i) & 1u) && c[i] > bc) { bc = c[i]; bv = v[i]; bi = i; }
+        const V m = wave_max(bc);
+        const bool near = !(last - m > 2 * eps);
+        if (m == -INFINITY || (n >= p.k && !near)) return n >= p.k;
+        const int o = __ffsll((unsigned long long)__ballot(bc == m)) - 1;
+        if (near) close |= 1ull << n;
+        if (lane == o) taken |= 1u << bi;
+        const int e = o + 64 * __builtin_amdgcn_readlane(bi, o);
+        const V ev = lane_value(bv, o);
+        if (lane == n) { my_e = e; my_c = m; my_v = ev; }
+        last = m;
+        ++n;
+    }
+    return false;
+}
+
+// Puts the slots (lane j: expert e, score pr, value c) in their fp64 order and
+// writes token t: the experts of close slots are summed again, shared out over the
+// work-group's waves.  ex: LDS [64].
+__device__ __forceinline__ void settle(const ScoredPass &p, int t, int wave, int lane, int slots, uint64_t close, int e, double pr,
+                                       double c, double *ex)
+{
+    uint64_t todo = close | close >> 1;
+    for (int i = 0; todo; ++i) {
+        const int j = __ffsll((unsigned long long)todo) - 1;
+        todo &= todo - 1;
+        if (i % EXACT_WAVES != wave) continue;
+        const double v = exact_logit(p, t, __builtin_amdgcn_readlane(e, j), lane);
+        if (lane == 0) ex[j] = v;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        if ((close | close >> 1) >> lane & 1) {
+            pr = sigmoid64(ex[lane]);
+            c = biased(p, e, ex[lane], pr);
+        }
+        int slot = lane < slots ? 0 : p.k;
+        for (int j = 0; j < slots; ++j) {
+            const double v = readlane_f64(c, j);
+            const int oe = __builtin_amdgcn_readlane(e, j);
+            if (lane < slots) slot += v > c || (v == c && oe < e);
+        }
+        write_token(p, t, slot, e, slot < p.k ? pr : 0.0);
+    }
+    __syncthreads();                             // ex is read
+}
+
 // The tokens that scored_split_topk left open, a work-group each.  Mostly it
 // names the experts around the top k in order, and which of them are too close to
-// their neighbours: those are summed in fp64, shared out over the waves, and
-// ordered again.  Otherwise every wave holds the whole token and goes the same
-// way: groups around the border are decided on fp64 values first, then every
-// expert that may be among the k largest.
+// their neighbours: those are settled in fp64.  Otherwise every wave holds the
+// whole token and goes the same way: groups around the border are decided on fp64
+// values first, then the slots; without a bound, or with more than 64 slots,
+// every expert that may be among the k largest is summed again.  8192 tokens of
+// 256 experts leave about 520 open, some 80 of them for their groups.
 template <int MAXPL>
 __global__ __launch_bounds__(64 * EXACT_WAVES) void scored_split_exact(ScoredPass p, int parts, float rounding)
 {
@@ -751,30 +822,9 @@ __global__ __launch_bounds__(64 * EXACT_WAVES) void scored_split_exact(ScoredPas
         const OpenToken &o = ((const OpenToken *)(p.open + 4))[at];
         const int t = o.t, slots = o.slots;
         if (slots > 0) {
-            const uint64_t close = o.close;
             const int e = lane < slots ? o.expert[lane] : 0;
-            double l = lane < slots ? (double)o.logit[lane] : -INFINITY;
-            uint64_t todo = close | close >> 1;
-            for (int i = 0; todo; ++i) {
-                const int j = __ffsll((unsigned long long)todo) - 1;
-                todo &= todo - 1;
-                if (i % EXACT_WAVES != wave) continue;
-                const double v = exact_logit(p, t, __builtin_amdgcn_readlane(e, j), lane);
-                if (lane == 0) ex[j] = v;
-            }
-            __syncthreads();
-            if (wave == 0) {
-                if ((close | close >> 1) >> lane & 1) l = ex[lane];
-                const double pr = sigmoid64(l), c = lane < slots ? biased(p, e, l, pr) : -INFINITY;
-                int slot = lane < slots ? 0 : p.k;
-                for (int j = 0; j < slots; ++j) {
-                    const double v = readlane_f64(c, j);
-                    const int oe = __builtin_amdgcn_readlane(e, j);
-                    slot += v > c || (v == c && oe < e);
-                }
-                write_token(p, t, slot, e, slot < p.k ? pr : 0.0);
-            }
-            __syncthreads();                     // ex is read
+            const double l = lane < slots ? (double)o.logit[lane] : -INFINITY, q = sigmoid64(l);
+            settle(p, t, wave, lane, slots, o.close, e, q, lane < slots ? biased(p, e, l, q) : -INFINITY, ex);
             continue;
         }
         double pr[MAXPL], c[MAXPL];
@@ -788,7 +838,7 @@ __global__ __launch_bounds__(64 * EXACT_WAVES) void scored_split_exact(ScoredPas
             c[i] = lane + 64 * i < p.E ? biased(p, lane + 64 * i, (double)l[i], pr[i]) : -INFINITY;
             if (!(eps < INFINITY) && lane + 64 * i < p.E) flags |= 1u << i;
         }
-        refine<MAXPL>(p, t, wave, lane, flags, done, pr, c, ex);
+        if (!(eps < INFINITY)) refine<MAXPL>(p, t, wave, lane, flags, done, pr, c, ex);
         if (p.keep < p.groups) {
             const float inv = 1.0f / (float)(p.E / p.groups);
             Groups<double> g = rank_groups<MAXPL, double>(p, lane, c, cs[wave]);
@@ -813,8 +863,13 @@ __global__ __launch_bounds__(64 * EXACT_WAVES) void scored_split_exact(ScoredPas
                     done |= 1u << i;
                 }
         }
-        int my_e;
+        int my_e, n_slots;
         double my_c, my_p;
+        uint64_t close;
+        if (eps < INFINITY && order_slots<MAXPL, double>(p, lane, c, pr, eps, my_e, my_c, my_p, n_slots, close)) {
+            settle(p, t, wave, lane, n_slots, close, my_e, my_p, my_c, ex);
+            continue;
+        }
         uint32_t taken;
         select64<MAXPL>(p, lane, c, pr, my_e, my_c, my_p, taken);
         const double least = readlane_f64(my_c, p.k - 1) - 2.0 * eps;
@@ -859,33 +914,11 @@ __global__ __launch_bounds__(64 * WAVES) void scored_split_topk(ScoredPass p, in
         for (int i = 0; i < MAXPL; ++i)
             if (!(g.kept >> group_of(min(lane + 64 * i, p.E - 1), inv) & 1)) c[i] = -INFINITY;
     }
-    // the largest values in order, lane j keeps slot j, down to the first past k
-    // that is certainly below its predecessor; bit j of close: slot j may not be
     int my_e = 0, n = 0;
-    float my_l = 0.0f, last = INFINITY;
+    float my_c, my_l = 0.0f;
     uint64_t close = 0;
-    uint32_t taken = 0;
-    bool end = false;                            // found that first one, or nothing is left
-    while (!open && n < 64) {
-        float bv = -INFINITY, bl = 0.0f;
-        int be = 0;
-#pragma unroll
-        for (int i = 0; i < MAXPL; ++i)
-            if (!((taken >> i) & 1u) && c[i] > bv) { bv = c[i]; bl = l[i]; be = i; }
-        const float m = wave_max_f32(bv);
-        const bool near = !(last - m > 2.0f * eps);
-        end = m == -INFINITY || (n >= p.k && !near);
-        if (end) break;
-        const int o = __ffsll((unsigned long long)__ballot(bv == m)) - 1;
-        if (near) close |= 1ull << n;
-        if (lane == o) taken |= 1u << be;
-        const int e = o + 64 * __builtin_amdgcn_readlane(be, o);
-        const float el = lane_value(bl, o);
-        if (lane == n) { my_e = e; my_l = el; }
-        last = m;
-        ++n;
-    }
-    open = open || !end || n < p.k;              // groups, no bound, too many close ones, too few experts
+    // else open: groups, no bound, too many close ones, too few experts
+    open = open || !order_slots<MAXPL, float>(p, lane, c, l, eps, my_e, my_c, my_l, n, close);
     if (!open && !close) {
         write_token(p, t, lane, my_e, lane < p.k ? sigmoid64((double)my_l) : 0.0);
         return;
@@ -1031,7 +1064,7 @@ hipError_t launch_scored_split_logits(const ScoredPass &p, hipStream_t s)
 
 hipError_t launch_scored_topk(const ScoredPass &p, hipStream_t s)
 {
-    const bool split = scored_split(p.T, p.softmax, p.x_bf16);
+    const bool split = scored_split(p.T, p.E, p.softmax, p.x_bf16);
     const int parts = split ? scored_split_parts(p.T, p.H, p.E)
                             : p.T <= SCORED_SMALL_T ? parts_small(p.H) : parts64(p.T, p.H, p.E);
     const int waves = p.T == 1 ? 1 : WAVES;

@@ -373,9 +373,9 @@ int moe_expert_cache_prefetch(moe_expert_cache *c, int layer_id, const moe_layer
  *   topk_w[t,j] = p_j * scale, with MOE_ROUTER_RENORM divided by sum_j' p_j'
  *   offsets, perm, inv: as moe_route
  * The selection is that of fp64 scores: no expert is chosen on a rounding of
- * fewer bits.  The weights are those of fp64 logits, or, for more than 64 bf16
- * tokens with sigmoid scores, of logits summed in fp32 pieces (within 2^-20 |x|
- * |w_e| of exact, in practice about 1e-7 of a logit's spread): a token's experts
+ * fewer bits.  The weights are those of fp64 logits, or, for large batches of
+ * bf16 tokens with sigmoid scores, of logits summed in fp32 pieces (within 2^-20
+ * |x| |w_e| of exact, in practice about 1e-7 of a logit's spread): a token's experts
  * do not depend on the batch it comes in, its weights only to that.  Where c = -inf (a bias of -inf, a group not kept, a NaN score,
  * which counts as p = 0 and c = -inf) an expert is chosen only if fewer than k
  * others are left, and then has weight 0; a token with nothing left gets k

@@ -395,7 +395,9 @@ ROUTE_CASES = [  # T, H, E, k, x, score, bias, groups, keep, renorm, padding
     (130, 72, 32, 4, F32, "sigmoid", 0.05, 4, 2, True, 0), (333, 1112, 160, 6, F32, "softmax", 0.001, 1, 1, False, 0),
     (500, 2048, 512, 10, BF16, "sigmoid", 0.02, 32, 8, True, 0), (257, 512, 1000, 16, BF16, "sigmoid", 0.02, 10, 9, True, 0),
     (1025, 1024, 256, 8, BF16, "softmax", None, 8, 4, True, 0), (2048, 7168, 256, 8, BF16, "sigmoid", 0.05, 8, 4, True, 0),
-    (3000, 256, 128, 8, BF16, "sigmoid", 0.05, 1, 1, True, 0),
+    (3000, 256, 128, 8, BF16, "sigmoid", 0.05, 1, 1, True, 0), (700, 7168, 256, 8, BF16, "sigmoid", 0.05, 8, 4, True, 8),
+    (1300, 1112, 160, 64, BF16, "sigmoid", 0.05, 4, 3, False, 0), (4200, 520, 40, 5, BF16, "sigmoid", None, 20, 7, True, 0),
+    (2600, 8, 64, 3, BF16, "sigmoid", 0.01, 16, 2, True, 0), (200, 4096, 1024, 8, BF16, "sigmoid", 0.02, 64, 60, True, 0),
 ]
 
 
@@ -406,7 +408,7 @@ def test_route_scored(T, H, E, k, xt, score, bias, groups, keep, renorm, pad):
     check_route(T, H, E, k, xt, score, bias, groups, keep, renorm, pad=pad)
 
 
-@pytest.mark.parametrize("T", [1, 3, 40, 200])
+@pytest.mark.parametrize("T", [1, 3, 40, 200, 2700])
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])
 def test_route_ties(T, score):
     """Equal router rows give equal scores: the lower expert and the lower group win."""
@@ -432,7 +434,7 @@ def test_route_near_ties(T):
         check_route(T, H, E, 8, BF16, "sigmoid", None, groups, keep, True, x=rnd(54, T, H, dtype=BF16), w=w)
 
 
-@pytest.mark.parametrize("T", [80, 2000])
+@pytest.mark.parametrize("T", [80, 2000, 2700])
 def test_route_scores_on_the_border(T):
     """Biases that bring every expert's selection value to within 1e-7 of 1 for one token's scores, so that the order
     turns on bits that fp32 sums do not have; groups as close."""
@@ -449,7 +451,7 @@ def test_route_scores_on_the_border(T):
         check_route(T, H, E, 8, BF16, "sigmoid", bias, groups, keep, True, x=xs, w=w)
 
 
-@pytest.mark.parametrize("T", [1, 5, 300])
+@pytest.mark.parametrize("T", [1, 5, 300, 5300])
 def test_route_masked_experts(T):
     """Experts masked by a bias of -inf, down to fewer than k and to none; NaN rows of x; very large scores."""
     need_gpu()
