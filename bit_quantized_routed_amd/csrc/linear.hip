@@ -376,7 +376,7 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void linear_tile(LinearPass p, int
 // 4 k + 3 (waves 0-3 wait there for all their loads, of w; waves 4-7 for all but
 // the newest eight, which are x of step k + 2).
 //
-// 8192 x 4096 x 7168: 198 us, 2.43 POP/s, where products alone take 143 us at the
+// 8192 x 4096 x 7168: 197 us, 2.44 POP/s, where products alone take 143 us at the
 // clock that the power limit leaves (4.2 POP/s), loads alone 105 us.  Tiles of
 // 32x32 products, one wave a SIMD with 128 x 128 outputs, and two buffers of a
 // whole step each were slower (239, 368, 222 us).
@@ -525,8 +525,8 @@ hipError_t launch_big(const LinearPass &p, hipStream_t s)
 // waves split K in slices of 512 bytes and load a slice of w straight into
 // registers as matrix operands (a lane's 16 bytes of K are the same for both
 // operands, whichever they are), every load of a slice in flight before the
-// first product.  The waves' integer sums meet in LDS.  1 x 4096 x 7168: 8.7 us,
-// 3.4 TB/s.
+// first product.  The waves' integer sums meet in LDS.  1 x 4096 x 7168: 7.0 us,
+// 4.2 TB/s.
 constexpr int SLICE = 8;                         // products of 64 bytes of K in a slice
 
 __global__ __launch_bounds__(1024) void linear_stream(LinearPass p)
@@ -593,9 +593,9 @@ hipError_t launch_tile(const LinearPass &p, int parts, hipStream_t s)
 // The kernel for a shape.  Measured costs of a step of 128 bytes of K (us, one
 // tile on a CU, and two at once where two fit) and of a tile's start and end;
 // the sizes are those of the tiles.  Larger tiles read the operands fewer
-// times, smaller ones fill the 256 CUs and lose less at ragged edges: at T =
-// 512, N = 4096, K = 7168 the variants take 92 / 52 / 29 / 32 us in this order,
-// at T = 8192 207 / 263 / 300 / 400 us.
+// times, smaller ones fill the 256 CUs and lose less at ragged edges: at N = 4096
+// and K = 7168 the variants take, in this order, 91 / 52 / 30 / 32 / 45 us for T =
+// 512, 91 / 68 / 86 / 111 us for 2048 and 201 / 250 / 314 / 388 / 518 us for 8192.
 struct Plan {
     int kernel, parts;                           // kernel: index below, or STREAM
 };
@@ -612,8 +612,8 @@ constexpr int CUS = 256, SPLIT_STEPS = 14;
 
 Plan plan_of(int T, int N, int K)
 {
-    // up to one fragment of tokens: w streams through registers once (1 x 4096
-    // x 7168: 8.7 us, against 13 of the smallest tile on 4 parts of K)
+    // up to one fragment of tokens: w streams through registers once (16 x 4096
+    // x 7168: 11 us, against 17 of the smallest tile and 13 of it on 4 parts of K)
     if (T <= 16) return {STREAM, 1};
     const int steps = (K + BK - 1) / BK;
     Plan best{0, 1};

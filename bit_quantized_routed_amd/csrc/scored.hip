@@ -238,7 +238,7 @@ __global__ __launch_bounds__(256) void scored_split_w(ScoredPass p, int rows)
 // smallest term's products are added first, sums run over 128 of H and are then
 // added to the totals, so that a logit has been rounded 12 times in its short sum
 // and once for each short sum.  Parts of H are dealt so that an XCD sees few of
-// them: its share of the terms stays in its L2.  8192 x 7168 x 256: 100 us for 90
+// them: its share of the terms stays in its L2.  8192 x 7168 x 256: 95 us for 90
 // Gflop of products (a large library product runs at 1.37 Pflop/s here, 66 us);
 // loads alone 50 us, products and LDS reads 75.  Alternating the waves of a SIMD
 // between reading and multiplying, as the int8 linear layer does, took 105 us.
@@ -606,7 +606,8 @@ struct OpenToken {
 };
 
 // fp64 selection; a single token is grouped here too (the sorted selection:
-// offsets from ballots of the taken flags)
+// offsets from ballots of the taken flags).  One token of 256 experts: 7.6 us, the
+// latency of the scores' exp, the groups' exchanges and k rounds of the maximum.
 template <int MAXPL>
 __global__ __launch_bounds__(64 * WAVES) void scored_topk(ScoredPass p, int parts)
 {
