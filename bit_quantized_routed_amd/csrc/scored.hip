@@ -736,7 +736,7 @@ __device__ __forceinline__ float value_error(const ScoredPass &p, int t, int par
     wmax = wave_max_f32(wmax);
     bmax = wave_max_f32(bmax);
     const float d = rounding * sqrtf(xn) * sqrtf(wmax);
-    return d < 1e-2f ? 0.25f * d + 0x1p-21f * (1.0f + bmax) : INFINITY;
+    return d < 1e30f ? 0.25f * d + 0x1p-21f * (1.0f + bmax) : INFINITY;
 }
 
 // The experts around the top k in order, lane j slot j with its expert, value c
@@ -754,7 +754,7 @@ __device__ __forceinline__ bool order_slots(const ScoredPass &p, int lane, const
     my_v = 0;
     n = 0;
     close = 0;
-    while (n < 64) {
+    while (true) {
         V bc = -INFINITY, bv = 0;
         int bi = 0;
 #pragma unroll
@@ -763,6 +763,7 @@ __device__ __forceinline__ bool order_slots(const ScoredPass &p, int lane, const
         const V m = wave_max(bc);
         const bool near = !(last - m > 2 * eps);
         if (m == -INFINITY || (n >= p.k && !near)) return n >= p.k;
+        if (n == 64) return false;
         const int o = __ffsll((unsigned long long)__ballot(bc == m)) - 1;
         if (near) close |= 1ull << n;
         if (lane == o) taken |= 1u << bi;
@@ -772,7 +773,6 @@ __device__ __forceinline__ bool order_slots(const ScoredPass &p, int lane, const
         last = m;
         ++n;
     }
-    return false;
 }
 
 // Puts the slots (lane j: expert e, score pr, value c) in their fp64 order and

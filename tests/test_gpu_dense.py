@@ -372,7 +372,7 @@ def check_route(T, H, E, k, xt, score, bias, groups, keep, renorm, seed=41, x=No
     # A weight is a smooth function of the logits, |d ln p / d l| <= 1 (sigmoid) or <= 2 times the largest logit's
     # (softmax), once more through the sum of the weights; a logit is off by at most 2^-20 |x| |w_e| (fp32 sums of
     # short stretches where many tokens share the matrix instructions).  One rounding to fp32 at the end.
-    xn = np.linalg.norm(np.nan_to_num(x.float().numpy(), posinf=0, neginf=0), axis=1, keepdims=True)
+    xn = np.linalg.norm(np.nan_to_num(x.double().numpy(), posinf=0, neginf=0), axis=1, keepdims=True)
     d = 2.0 ** -20 * xn * np.linalg.norm(w.numpy(), axis=1).max()
     gw = r.topk_w.cpu().numpy().astype(np.float64)
     assert np.all(np.abs(gw - wt) <= wt * (1.01 * H24 + 4 * d) + 1e-44)
@@ -449,6 +449,17 @@ def test_route_scores_on_the_border(T):
     xs[1::2] = rnd(60, T // 2, H, dtype=BF16)
     for groups, keep in ((1, 1), (8, 4)):
         check_route(T, H, E, 8, BF16, "sigmoid", bias, groups, keep, True, x=xs, w=w)
+
+
+@pytest.mark.parametrize("T,std", [(3000, 60.0), (3000, 1e-4), (2800, 1e30), (60, 60.0)])
+def test_route_large_and_small_logits(T, std):
+    """Logits far from the sigmoid's slope on both sides, with saturated scores that tie, and nearly equal ones."""
+    need_gpu()
+    say("route scale", T, std)
+    x = rnd(63, T, 128, std=std, dtype=BF16)
+    for groups, keep in ((1, 1), (8, 4)):
+        check_route(T, 128, 64, 8, BF16, "sigmoid", None, groups, keep, False, x=x)
+    check_route(T, 128, 64, 64, BF16, "sigmoid", 0.05, 1, 1, True, x=x)
 
 
 @pytest.mark.parametrize("T", [1, 5, 300, 5300])
