@@ -782,6 +782,7 @@ __device__ __forceinline__ void settle(const ScoredPass &p, int t, int wave, int
                                        double c, double *ex)
 {
     uint64_t todo = close | close >> 1;
+    __syncthreads();                             // ex is read: by refine for this token, by this function or refine for the last
     for (int i = 0; todo; ++i) {
         const int j = __ffsll((unsigned long long)todo) - 1;
         todo &= todo - 1;
@@ -803,7 +804,6 @@ __device__ __forceinline__ void settle(const ScoredPass &p, int t, int wave, int
         }
         write_token(p, t, slot, e, slot < p.k ? pr : 0.0);
     }
-    __syncthreads();                             // ex is read
 }
 
 // The tokens that scored_split_topk left open, a work-group each.  Mostly it
