@@ -374,9 +374,11 @@ int moe_expert_cache_prefetch(moe_expert_cache *c, int layer_id, const moe_layer
  *   offsets, perm, inv: as moe_route
  * The selection is that of fp64 scores: no expert is chosen on a rounding of
  * fewer bits.  The weights are those of fp64 logits, or, for large batches of
- * bf16 tokens with sigmoid scores, of logits summed in fp32 pieces (within 2^-20
- * |x| |w_e| of exact, in practice about 1e-7 of a logit's spread): a token's experts
- * do not depend on the batch it comes in, its weights only to that.  Where c = -inf (a bias of -inf, a group not kept, a NaN score,
+ * bf16 tokens with sigmoid scores, of logits summed in fp32 pieces (off by at most
+ * 2^-24 (60 + hidden / 128) |x| |w_e|, in practice about 1e-7 of a logit's spread): a
+ * token's weights depend on the batch it comes in to that, its experts only where
+ * selection values agree to fp64's own roundings, as fp64 logits are summed in an
+ * order that hangs on the batch's size (equal rows of w_router tie in all).  Where c = -inf (a bias of -inf, a group not kept, a NaN score,
  * which counts as p = 0 and c = -inf) an expert is chosen only if fewer than k
  * others are left, and then has weight 0; a token with nothing left gets k
  * weights of 0.  (A logit of +inf has sigmoid 1, and all of the softmax,
