@@ -741,7 +741,9 @@ __device__ __forceinline__ float value_error(const ScoredPass &p, int t, int par
     for (int q = 0; q < parts; ++q) xn += p.xnorm[(int64_t)q * p.T + t];
     wmax = wave_max_f32(wmax);
     bmax = wave_max_f32(bmax);
-    const float d = rounding * sqrtf(xn) * sqrtf(wmax);
+    // squares below fp32's smallest are missing from both sums, of less than 2^-126 each even where they are flushed
+    const float lost = 0x1p-126f * (float)p.H;
+    const float d = rounding * sqrtf(xn + lost) * sqrtf(wmax + lost);
     return d < 1e30f ? 0.25f * d + 0x1p-21f * (1.0f + bmax) : INFINITY;
 }
 

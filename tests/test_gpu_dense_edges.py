@@ -57,14 +57,14 @@ def uneven_sums(sign, rng):
     return x, w
 
 
-def uneven_router(scale):
-    """(x [264], w [264]): x w = 0, with every rounding of its parts' sums upwards."""
+def uneven_router(scale, pairs=1, w_scale=1.0):
+    """(x, w) of 256 pairs + 8 of H: x w = 0, with every rounding of its parts' sums upwards."""
     rng = np.random.default_rng(1)
-    (xa, wa), (xb, wb) = uneven_sums(1, rng), uneven_sums(-1, rng)
-    x, w = np.concatenate([xa, xb, np.zeros(8)]), np.concatenate([wa, wb, np.zeros(8)])
-    x[256], w[256] = 2.0 ** -4, -16 * float(x @ w)
-    x, w = torch.from_numpy(x * scale).bfloat16(), torch.from_numpy(w).float()
-    assert abs(float(x.double() @ w.double())) < 2.0 ** -24 * scale
+    parts = [uneven_sums(sign, rng) for _ in range(pairs) for sign in (1, -1)] + [(np.zeros(8), np.zeros(8))]
+    x, w = (np.concatenate([p[i] for p in parts]) for i in (0, 1))
+    x[-8], w[-8] = 2.0 ** -4, -16 * float(x @ w)
+    x, w = torch.from_numpy(x * scale).bfloat16(), torch.from_numpy(w * w_scale).float()
+    assert abs(float(x.double() @ w.double())) < 2.0 ** -24 * scale * w_scale
     return x, w
 
 
@@ -143,3 +143,21 @@ def test_route_split_weights_at_worst_roundings():
     off, bound = np.abs(got - wt) / wt, split_bound(xs, w, idx, 264)
     say("off by", off.max(), "of", bound.max(), "in units of 2^-24 |x| |w|:", 2 * off.max() * (60 + 3) / bound.max())
     assert np.all(off <= 1.01 * H24 + bound)
+
+
+@pytest.mark.parametrize("scale,w_scale", [(2.0 ** -64, 2.0 ** 60), (2.0 ** -60, 2.0 ** 60), (2.0 ** 60, 2.0 ** -64), (2.0 ** 60, 2.0 ** -68)])
+def test_route_squares_below_the_smallest_float(scale, w_scale):
+    """Ordinary logits of tokens (or router rows) whose elements have squares that fp32 does not hold, against large rows
+    (or tokens): the worst roundings still leave the order to fp64."""
+    need_gpu()
+    say("route small squares", scale, w_scale)
+    T, E, pairs = 2700, 64, 32
+    x, row = uneven_router(scale, pairs, w_scale)
+    w = torch.zeros((E, len(x)))
+    w[20], w[40] = row, -row
+    p = 1 / (1 + np.exp(-np.array([1.0, -1.0]) * float(x.double() @ row.double())))
+    bias = torch.full((E,), -0.25)
+    bias[20] = 0.0
+    bias[40] = float(np.float32(p[0] - p[1] + 1e-9))
+    r, _ = check_route(T, len(x), E, 1, BF16, "sigmoid", bias, 1, 1, True, x=x.repeat(T, 1), w=w)
+    assert int(r.topk_idx[0, 0]) == 40
