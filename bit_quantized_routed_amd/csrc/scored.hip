@@ -541,7 +541,8 @@ __device__ __forceinline__ Groups<V> rank_groups(const ScoredPass &p, int lane, 
             a = fmax(a, v);
         }
     }
-    g.score = size > 1 ? a + b : a;
+    // inf - inf would be a NaN, which no score outranks
+    g.score = size == 1 ? a : b == -INFINITY ? b : a + b;
     g.second = size > 1 ? b : a;
     int r = 0;
     for (int o = 0; o < G; ++o) {

@@ -367,8 +367,10 @@ int moe_expert_cache_prefetch(moe_expert_cache *c, int layer_id, const moe_layer
  *   p[t,e] = 1/(1+exp(-l))  (MOE_SCORE_SIGMOID)  or  exp(l) / sum_e' exp(l)  (MOE_SCORE_SOFTMAX)
  *   c[t,e] = p[t,e] + bias[e]       (bias fp32 [E], device, or NULL)
  *   group g holds experts g*E/n_groups .. ; its score is the sum of its two
- *     largest c (its one c if it holds one expert); the keep_groups groups of
- *     the largest score stay (ties to the lower group), in the others c = -inf
+ *     largest c (its one c if it holds one expert; -inf if fewer than two are above
+ *     -inf, whatever the other); the keep_groups groups of the largest score stay
+ *     (ties to the lower group), in the others c = -inf.  Routers that rank groups
+ *     by their single largest score are not covered.
  *   topk_idx[t,0..k) = the k largest c[t,:], descending, ties to the lower e
  *   topk_w[t,j] = p_j * scale, with MOE_ROUTER_RENORM divided by sum_j' p_j'
  *   offsets, perm, inv: as moe_route

@@ -161,3 +161,23 @@ def test_route_squares_below_the_smallest_float(scale, w_scale):
     bias[40] = float(np.float32(p[0] - p[1] + 1e-9))
     r, _ = check_route(T, len(x), E, 1, BF16, "sigmoid", bias, 1, 1, True, x=x.repeat(T, 1), w=w)
     assert int(r.topk_idx[0, 0]) == 40
+
+
+@pytest.mark.parametrize("T", [1, 100, 900, 5300])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_groups_of_one_forced_expert(T, score):
+    """A group with one expert of bias +inf and all others at -inf holds fewer than two that can be chosen: its score is
+    -inf, and exactly `keep` groups stay."""
+    need_gpu()
+    say("route forced", T, score)
+    H, E, inf = 128, 64, float("inf")
+    bias = rnd(131, E, std=0.01)
+    bias[8:16] = -inf
+    bias[11] = inf
+    bias[40:48] = -inf                             # nothing left
+    bias[50:56] = -inf                             # two left
+    x, w = rnd(132, T, H, dtype=BF16), rnd(133, E, H, std=H ** -0.5)
+    with np.errstate(invalid="ignore"):
+        r, _ = check_route(T, H, E, 8, BF16, score, bias, 8, 3, True, x=x, w=w)
+    group = r.topk_idx.cpu().numpy() // 8
+    assert not np.isin(group, [1, 5]).any() and all(len(set(g)) <= 3 for g in group)
