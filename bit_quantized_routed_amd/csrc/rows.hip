@@ -85,19 +85,24 @@ __device__ __forceinline__ void store8(void *p, int bf16, int c, int step, int n
 // one Newton step: off by at most 7 half units in the last place (3 of the
 // exponential, the sum, the reciprocal and two products), in half the
 // instructions of expf and a division (8192 x 2048: 22 us with those, bound by
-// arithmetic).  The exponent stops at 126, where silu is below 2^-119 of u: the
-// reciprocal's argument stays finite.
+// arithmetic).  Past p = 125 the 1 of the sum is below its last place: it is left
+// out, the exponential is taken 2^120 smaller (p - 120 is exact) and u too, so that
+// all stays normal; and from a = -170.5 on silu is below 2^-238, which with the
+// largest u is below half a code of any row that has codes: zero there.  The
+// exponential's argument stops at 170.5 either way (silu(a) is a by then).
 __device__ __forceinline__ float silu_mul(float a, float u)
 {
+#pragma clang fp contract(off)                   // t is what p's own rounding lost
     constexpr float L = 1.44269502f, L_REST = 1.92596303e-8f, LN2 = 0.693147182f;   // log2 e in two parts, ln 2
-    const float p = fminf(-a * L, 126.0f);
-    const float t = fmaf(-a, L_REST, fmaf(-a, L, a * L));
-    float e = __builtin_amdgcn_exp2f(p);
-    e = p < 126.0f ? fmaf(e, t * LN2, e) : e;
-    const float d = 1.0f + e;
+    const float b = __builtin_amdgcn_fmed3f(-a, -170.5f, 170.5f), p = b * L;
+    const float t = fmaf(b, L_REST, fmaf(b, L, -p));
+    const bool far = p > 125.0f;
+    float e = __builtin_amdgcn_exp2f(far ? p - 120.0f : p);
+    e = fmaf(e, t * LN2, e);
+    const float d = far ? e : 1.0f + e;
     float r = __builtin_amdgcn_rcpf(d);
     r = fmaf(fmaf(-d, r, 1.0f), r, r);
-    return a * r * u;
+    return a * r * (a <= -170.5f ? u * 0.0f : far ? u * 0x1p-120f : u);
 }
 
 // rint(v * inv), |v * inv| < 2^22, in the low bits: the sum's spacing is 1

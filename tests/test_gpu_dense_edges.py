@@ -181,3 +181,53 @@ def test_route_groups_of_one_forced_expert(T, score):
         r, _ = check_route(T, H, E, 8, BF16, score, bias, 8, 3, True, x=x, w=w)
     group = r.topk_idx.cpu().numpy() // 8
     assert not np.isin(group, [1, 5]).any() and all(len(set(g)) <= 3 for g in group)
+
+
+# ------------------------------------------------------------------ rows to int8
+def exact_swiglu(x):
+    a, b = x.double().chunk(2, 1)
+    return a / (1 + torch.exp(-a)) * b
+
+
+@pytest.mark.parametrize("xt", [F32, BF16])
+@pytest.mark.parametrize("K", [64, 200, 1003])
+def test_swiglu_of_large_gates(xt, K):
+    """Finite gates up to the type's largest, either sign, with `up` from small to as large as the product allows."""
+    need_gpu()
+    say("swiglu large", xt, K)
+    big = float(torch.finfo(xt).max)
+    rows = [(lo, hi, up) for lo, hi, up in (
+        (80.0, 90.0, 1.0), (100.0, 200.0, 1e-3), (1e4, 2e4, 1.0), (1e31, 2e31, 1.0), (1e38, 2e38, 0.25), (2.4e38, 3.3e38, 1e-5),
+        (big, big, 0.125), (-85.0, -80.0, 1.0), (-89.5, -86.0, 1e20), (-95.0, -87.0, 1e30), (-130.0, -100.0, 1e35),
+        (-160.0, -140.0, 1e38), (-175.0, -165.0, 1e38), (-300.0, -200.0, 1e38), (-1.1e4, -1e4, 1.0), (-2e31, -1e31, 1e30),
+        (-2e38, -1e38, 1.0), (-big, -big, 1e38), (-big, -big, 1.0))]
+    g = torch.Generator().manual_seed(141)
+    x = torch.empty((len(rows), 2 * K), dtype=xt)
+    for i, (lo, hi, up) in enumerate(rows):
+        x[i, :K] = (lo + (hi - lo) * torch.rand(K, generator=g)).clamp(-big, big).to(xt)
+        x[i, K:] = (torch.rand(K, generator=g) * 2 - 1).mul(up).to(xt)
+    q, qs = M.empty_i8(len(rows), K), torch.empty(len(rows), device="cuda")
+    M.quant_i8(x.cuda(), q, qs, True)
+    v = exact_swiglu(x)
+    assert v.abs().max() < 3e38
+    qs, q = qs.cpu().double(), q.cpu().double()
+    amax = v.abs().amax(1)
+    for i, r in enumerate(rows):                   # the quantizer's rule: rows below 2^-100 are zero
+        if amax[i] < 2.0 ** -100 * (1 - 2.0 ** -20):
+            assert float(qs[i]) == 0 and int(q[i].abs().max()) == 0, r
+        elif amax[i] > 2.0 ** -100 * (1 + 2.0 ** -20):
+            # as test_quant_i8: seven half units for the value, two roundings of the scale, three of the code
+            assert abs(float(qs[i]) - float(amax[i]) / 127) <= 9.01 * H24 * float(amax[i]) / 127, r
+            assert float((q[i] - v[i] * (127 / amax[i])).abs().max()) <= 0.5 + 127 * (14.02 + 3) * H24, r
+
+
+def test_swiglu_marks_infinite_gates():
+    need_gpu()
+    say("swiglu marks")
+    x = rnd(142, 7, 128)
+    inf, nan = float("inf"), float("nan")
+    x[0, 3], x[1, 3], x[2, 3], x[3, 64 + 3], x[4, 64 + 3] = inf, -inf, nan, inf, nan
+    x[5, 3], x[5, 64 + 3] = -1e38, inf             # -0 * inf
+    q, qs = M.empty_i8(7, 64), torch.empty(7, device="cuda")
+    M.quant_i8(x.cuda(), q, qs, True)
+    assert torch.isnan(qs[:6]).all() and int(q[:6].abs().max()) == 0 and torch.isfinite(qs[6])
