@@ -6,6 +6,10 @@
 
 #include <algorithm>
 
+// the products with the scales, the bias and the addition each round to fp32, in
+// every kernel alike: no fma of two of them
+#pragma clang fp contract(off)
+
 namespace moe {
 
 namespace {

@@ -231,3 +231,35 @@ def test_swiglu_marks_infinite_gates():
     q, qs = M.empty_i8(7, 64), torch.empty(7, device="cuda")
     M.quant_i8(x.cuda(), q, qs, True)
     assert torch.isnan(qs[:6]).all() and int(q[:6].abs().max()) == 0 and torch.isfinite(qs[6])
+
+
+# ------------------------------------------------------------------ int8 linear
+@pytest.mark.parametrize("T,N,K,yt,bias,add,pad", [
+    (1, 4096, 1024, F32, True, False, 0), (7, 1003, 600, F32, True, True, 1), (16, 512, 512, BF16, True, True, 0),
+    (32, 512, 8192, F32, True, False, 0), (40, 1003, 8192, F32, True, True, 1), (32, 7168, 2048, F32, True, True, 0),
+    (333, 1003, 1111, F32, True, False, 0), (300, 512, 640, BF16, True, True, 0), (2048, 2048, 512, F32, True, False, 0),
+    (2100, 1101, 700, F32, True, True, 3), (4096, 4096, 384, F32, True, False, 0), (4096, 4095, 384, F32, True, True, 0),
+    (2048, 7168, 512, BF16, True, False, 0), (128, 256, 100, F32, False, True, 0)])
+def test_linear_rounds_as_stated(T, N, K, yt, bias, add, pad):
+    """The scales' product, the sum's product with it, the bias and the addition each round to fp32, in every kernel:
+    the same bits as these operations one after another."""
+    need_gpu()
+    say("linear bits", T, N, K, yt, bias, add, pad)
+    g = torch.Generator(device="cuda").manual_seed(151)
+
+    def codes(rows):
+        return torch.randint(-128, 128, (rows, (K + 15) // 16 * 16), generator=g, device="cuda", dtype=torch.int8)[:, :K]
+
+    x, w = codes(T), codes(N)
+    xs, ws = (torch.rand(n, generator=g, device="cuda") * 0.01 for n in (T, N))
+    b = torch.randn(N, generator=g, device="cuda") if bias else None
+    a = torch.randn((T, N), generator=g, device="cuda").to(yt) if add else None
+    lin = M.LinearI8(w, ws, b)
+    y = torch.empty((T, N + pad), dtype=yt, device="cuda")[:, :N]
+    M.linear_i8(lin, x, xs, y, a, lin.workspace(T))
+    v = torch.mm(x.double().contiguous(), w.double().t().contiguous()).float() * (xs[:, None] * ws[None, :])
+    if bias:
+        v = v + b
+    if add:
+        v = v + a.float()
+    assert torch.equal(y, v.to(yt))
