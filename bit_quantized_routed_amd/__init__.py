@@ -514,7 +514,7 @@ class LinearI8:
         return cls(w, scale, bias)
 
     def workspace(self, T: int, device="cuda"):
-        """A workspace for T tokens (empty where none is needed)."""
+        """A workspace for up to T tokens (empty where none is needed)."""
         import torch
         return torch.empty(int(lib().moe_linear_i8_workspace_bytes(self.ref, T)), dtype=torch.uint8, device=device)
 
@@ -552,7 +552,7 @@ class RouterWeights:
         self.ref = ctypes.byref(self.c)
 
     def workspace(self, T: int, device="cuda"):
-        """A workspace for T tokens of either activation type."""
+        """A workspace for up to T tokens of either activation type."""
         import torch
         n = int(lib().moe_route_scored_workspace_bytes(self.ref, T))
         return torch.empty(max(n, 256), dtype=torch.uint8, device=device)

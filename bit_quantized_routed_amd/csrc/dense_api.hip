@@ -126,11 +126,21 @@ size_t moe_route_scored_workspace_bytes(const moe_router *R, int T)
     p.T = T; p.H = R->hidden; p.E = R->n_experts; p.k = R->top_k;
     p.softmax = R->score == MOE_SCORE_SOFTMAX;
     size_t most = 0;
-    for (int bf16 = 0; bf16 < 2; ++bf16) {       // enough for either activation type
-        p.x_bf16 = bf16;
-        const size_t b = scored_ws(p, nullptr);
-        most = b > most ? b : most;
-    }
+    auto count = [&](int t) {
+        p.T = t;
+        for (int bf16 = 0; bf16 < 2; ++bf16) {   // enough for either activation type
+            p.x_bf16 = bf16;
+            const size_t b = scored_ws(p, nullptr);
+            most = b > most ? b : most;
+        }
+    };
+    // ... and for every smaller batch: H is cut into parts by whole tiles of 64 and
+    // 128 tokens, and not at all past 512 of the smaller ones, so what a call needs
+    // grows from one multiple of 64 to the next but where the split router begins
+    count(T);
+    for (int t = 64; t < T && t <= 64 * 512; t += 64) count(t);
+    const int last = scored_split_above(p.E);
+    if (last < T) count(last);
     return most;
 }
 
@@ -261,7 +271,7 @@ int moe_linear_i8(const moe_linear *W, int T, const int8_t *x, int64_t ldx, cons
     // a launch holds fewer than 2^32 threads: tiles of at least 32 x 64 with 256 threads, 16 channels with 1024
     if (((int64_t)T + 31) / 32 * (((int64_t)N + 63) / 64) >= ((int64_t)1 << 24) || N >= 1 << 26)
         return set_error(MOE_ERR_UNSUPPORTED, "T=%d x out_features=%d: too many tiles for one call", T, N);
-    const size_t need = linear_ws_bytes(T, N, K);
+    const size_t need = linear_needs_ws(T, N, K) ? linear_ws_bytes(T, N, K) : 0;
     if (need && !ws) return set_error(MOE_ERR_INVALID_ARG, "workspace is NULL");
     if ((uintptr_t)ws % 16) return set_error(MOE_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");
     if (ws_bytes < need) return set_error(MOE_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);

@@ -17,7 +17,8 @@ struct LinearPass {
     void *ws;
 };
 
-size_t linear_ws_bytes(int T, int N, int K);
+size_t linear_ws_bytes(int T, int N, int K);     // enough for up to T tokens
+bool linear_needs_ws(int T, int N, int K);       // whether T tokens use it
 hipError_t launch_linear(const LinearPass &p, hipStream_t s);
 
 }  // namespace moe

@@ -643,11 +643,19 @@ Plan plan_of(int T, int N, int K)
 
 }  // namespace
 
+// A bound of the parts' sums that grows with T, so that a workspace serves every
+// smaller batch too, of whichever plan: no more parts than plan_of makes of K, and
+// no more than CUS tiles in all of at most 128 x 128.  Past 128 x 128 channels
+// every tile row is more than half the CUs: no parts.
 size_t linear_ws_bytes(int T, int N, int K)
 {
-    const Plan plan = plan_of(T, N, K);
-    return plan.parts > 1 ? (size_t)plan.parts * T * N * sizeof(int32_t) : 0;
+    int parts = 1;
+    while ((K + BK - 1) / BK / (parts * 2) >= SPLIT_STEPS) parts *= 2;
+    if (T <= 16 || parts == 1 || N > 128 * 128) return 0;
+    return std::min<size_t>((size_t)parts * T * N, (size_t)CUS * 128 * 128) * sizeof(int32_t);
 }
+
+bool linear_needs_ws(int T, int N, int K) { return plan_of(T, N, K).parts > 1; }
 
 hipError_t launch_linear(const LinearPass &p, hipStream_t s)
 {

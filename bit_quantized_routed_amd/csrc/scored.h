@@ -32,10 +32,8 @@ constexpr int SCORED_SMALL_T = 128;
 // fp64 matrix instructions only reach past 640 tokens of 256 experts: H = 7168,
 // T = 333 / 500 / 700 / 1000 / 1400 / 2048 take 64 / 66 / 93 / 94 / 160 / 165 us
 // in fp64 and 83 / 85 / 87 / 89 / 93 / 94 us split.
-inline bool scored_split(int T, int E, bool softmax, bool x_bf16)
-{
-    return T > SCORED_SMALL_T && (int64_t)T * E > 640 * 256 && !softmax && x_bf16;
-}
+inline int scored_split_above(int E) { return 640 * 256 / E > SCORED_SMALL_T ? 640 * 256 / E : SCORED_SMALL_T; }
+inline bool scored_split(int T, int E, bool softmax, bool x_bf16) { return T > scored_split_above(E) && !softmax && x_bf16; }
 
 size_t scored_logit_bytes(int T, int H, int E, bool split);
 size_t scored_split_bytes(int H, int E);         // of wsplit

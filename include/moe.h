@@ -389,7 +389,7 @@ int moe_expert_cache_prefetch(moe_expert_cache *c, int layer_id, const moe_layer
  * n_groups <= 64 divides E, hidden H a multiple of 8.  x: [T] rows of H elements of
  * type act, ldx elements apart; x, w_router ([E][H] fp32) and ws 16-byte
  * aligned, ldx a multiple of 8.  Workspace: moe_route_scored_workspace_bytes()
- * (0 if R is invalid). */
+ * (0 if R is invalid); it serves every batch of up to T tokens. */
 enum moe_score { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
 #define MOE_ROUTER_RENORM 1
 typedef struct moe_router {
@@ -451,7 +451,8 @@ int moe_quant_i8(const void *x, int act, int64_t ldx, int T, int K, int flags, i
  *   a row are read and may hold anything.  y, add: element-aligned, strides in
  *   elements.
  *   Workspace: moe_linear_i8_workspace_bytes() (may be 0, then ws may be NULL;
- *   it never needs clearing); ws 16-byte aligned. */
+ *   it never needs clearing); it serves every batch of up to T tokens.  ws 16-byte
+ *   aligned. */
 typedef struct moe_linear {
     int32_t in_features, out_features; /* K, N */
     int64_t ldw;

@@ -263,3 +263,36 @@ def test_linear_rounds_as_stated(T, N, K, yt, bias, add, pad):
     if add:
         v = v + a.float()
     assert torch.equal(y, v.to(yt))
+
+
+# ------------------------------------------------------------------ one workspace for all batches
+def test_linear_workspace_of_the_largest_batch():
+    need_gpu()
+    say("linear workspace")
+    N, K, most = 256, 7168, 2000
+    g = torch.Generator(device="cuda").manual_seed(161)
+    x, w = (torch.randint(-128, 128, (n, K), generator=g, device="cuda", dtype=torch.int8) for n in (most, N))
+    lin = M.LinearI8(w, torch.ones(N, device="cuda"))
+    ws, ones = lin.workspace(most), torch.ones(most, device="cuda")
+    want = torch.mm(x.double(), w.double().t().contiguous())
+    for T in (1, 17, 32, 64, 100, 300, 512, 1000, 1999, 2000):
+        ws.fill_(0x55)
+        y = torch.empty((T, N), device="cuda")
+        M.linear_i8(lin, x[:T], ones[:T], y, ws=ws)
+        assert torch.equal(y, want[:T].float()), T
+
+
+@pytest.mark.parametrize("xt,score", [(BF16, "sigmoid"), (F32, "sigmoid"), (BF16, "softmax")])
+def test_router_workspace_of_the_largest_batch(xt, score):
+    need_gpu()
+    say("router workspace", xt, score)
+    H, E, k, most = 512, 256, 4, 4200
+    x, w = rnd(171, most, H, dtype=xt), rnd(172, E, H, std=H ** -0.5)
+    R = M.RouterWeights(w.cuda(), k, score)
+    ws, xd = R.workspace(most), x.cuda()
+    idx, _ = plain_route(x.float().numpy(), w.numpy(), k, score, None, 1, 1, True, 1.0)
+    for T in (1, 128, 129, 320, 640, 641, 1152, 1153, 1984, 2688, 4033, 4200):
+        ws.fill_(0x55)
+        r = M.Routing(T, k, E)
+        M.route_scored(R, xd[:T], r, ws)
+        assert np.array_equal(r.topk_idx.cpu().numpy(), idx[:T]), T
