@@ -243,7 +243,8 @@ struct Tile {
     static constexpr int BN = 16 * FA * WA, BM = 16 * FB * WB, NW = WA * WB, NT = 64 * NW;
     static constexpr int XB = BM * BK, WBYTES = BN * BK, SLOT = XB + WBYTES, LDS = RING * SLOT;
     static constexpr int LX = BM / 8 / NW, LW = BN / 8 / NW;   // loads of a wave in a step
-    static constexpr int SH = FA == 8 ? 5 : FA == 4 ? 4 : FA == 2 ? 3 : 2;   // log2(4 FA)
+    static constexpr int SH = FA == 4 ? 4 : 3;                 // log2(4 FA)
+    static_assert(4 * FA == 1 << SH, "four or two fragments");
     static_assert(LX * 8 * NW == BM && LW * 8 * NW == BN, "whole loads");
     static __device__ __forceinline__ int xkey(int r) { return r & 7; }
     static __device__ __forceinline__ int wkey(int r) { return (r & 3) | (((r >> SH) & 1) << 2); }
