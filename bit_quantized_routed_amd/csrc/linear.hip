@@ -381,8 +381,9 @@ __global__ __launch_bounds__(64 * WA * WB, 2) void linear_tile(LinearPass p, int
 // 4 k + 3 (waves 0-3 wait there for all their loads, of w; waves 4-7 for all but
 // the newest eight, which are x of step k + 2).
 //
-// 8192 x 4096 x 7168: 197 us, 2.44 POP/s, where products alone take 143 us at the
-// clock that the power limit leaves (4.2 POP/s), loads alone 105 us.  Tiles of
+// 8192 x 4096 x 7168: 198 us, 2.43 POP/s at 1.84 to 2.02 GHz (a kernel bound by
+// memory runs at 2.4), where products alone take 143 us (4.2 POP/s at the clock they
+// leave), loads alone 105 us.  Tiles of
 // 32x32 products, one wave a SIMD with 128 x 128 outputs, and two buffers of a
 // whole step each were slower (239, 368, 222 us).
 namespace big {
@@ -597,10 +598,11 @@ hipError_t launch_tile(const LinearPass &p, int parts, hipStream_t s)
 
 // The kernel for a shape.  Measured costs of a step of 128 bytes of K (us, one
 // tile on a CU, and two at once where two fit) and of a tile's start and end;
-// the sizes are those of the tiles.  Larger tiles read the operands fewer
-// times, smaller ones fill the 256 CUs and lose less at ragged edges: at N = 4096
-// and K = 7168 the variants take, in this order, 91 / 52 / 30 / 32 / 45 us for T =
-// 512, 91 / 68 / 86 / 111 us for 2048 and 201 / 250 / 314 / 388 / 518 us for 8192.
+// the sizes are those of the tiles, the times those of N = 4096 and K = 7168.
+// Larger tiles read the operands fewer times, smaller ones fill the 256 CUs and
+// lose less at ragged edges: there the variants take, in this order, 91 / 52 / 30 /
+// 32 / 45 us for T = 512, 91 / 68 / 86 / 111 us for 2048 and 201 / 250 / 314 / 388 /
+// 518 us for 8192.
 struct Plan {
     int kernel, parts;                           // kernel: index below, or STREAM
 };

@@ -13,9 +13,15 @@
 // next to a rounding border does.  The maximum is an integer maximum over the
 // magnitudes' bits, which an infinity or a NaN wins, so a row that holds one is seen.
 //
-// 8192 x 7168, fp32 x + bf16 residual to sum, bf16 and codes: 113 us, 5.7 TB/s (a
+// 8192 x 7168, fp32 x + bf16 residual to sum, bf16 and codes: 114 us, 5.7 TB/s (a
 // 1 GiB copy runs at 4.8 TB/s: the norm reads more than it writes).  8192 x 2048
-// SwiGLU from bf16: 17 us, 4.9 TB/s.  One row: 4.2 us and 2.3 us, latency.
+// SwiGLU from bf16: 17 us, 4.9 TB/s.  One row: 4.3 us and 2.3 us, latency.
+//
+// Rows that are not aligned go element by element: 227 us and 31 us for the same
+// two.  The longest rows do not fit the registers, and what is over goes through
+// scratch memory: the norm past 32768 (1024 x 65536: 470 us, 1.6 TB/s; a few
+// registers from 16384 on, 2048 x 32768: 164 us, 4.5 TB/s) and unaligned rows past
+// 16384 (norm) or 32768 (1024 x 65536: norm 846 us, codes 124 us).
 #include "common.h"
 #include "rows.h"
 

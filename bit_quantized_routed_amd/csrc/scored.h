@@ -30,8 +30,10 @@ constexpr int SCORED_SMALL_T = 128;
 // The split router (see scored.hip): bf16 tokens with sigmoid scores, and enough
 // of them.  Its launches have a floor (the terms of w, the open tokens) that the
 // fp64 matrix instructions only reach past 640 tokens of 256 experts: H = 7168,
-// T = 333 / 500 / 700 / 1000 / 1400 / 2048 take 64 / 66 / 93 / 94 / 160 / 165 us
-// in fp64 and 83 / 85 / 87 / 89 / 93 / 94 us split.
+// T = 333 / 500 / 640 / 700 / 1000 / 1400 / 2048 take 65 / 67 / 92 / 93 / 94 / 160
+// / 165 us in fp64 and 83 / 85 / 89 / 89 / 89 / 92 / 95 us split.  The border is
+// that of H = 7168: with H = 1024, T = 640 takes 34 us in fp64 and 59 split; with
+// H = 2048 and 64 experts T = 2560 takes 52 us either way.
 inline int scored_split_above(int E) { return 640 * 256 / E > SCORED_SMALL_T ? 640 * 256 / E : SCORED_SMALL_T; }
 inline bool scored_split(int T, int E, bool softmax, bool x_bf16) { return T > scored_split_above(E) && !softmax && x_bf16; }
 

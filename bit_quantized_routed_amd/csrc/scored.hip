@@ -238,7 +238,7 @@ __global__ __launch_bounds__(256) void scored_split_w(ScoredPass p, int rows)
 // smallest term's products are added first, sums run over 128 of H (12
 // instructions) and are then added to the totals, which keeps their roundings
 // few (value_error).  Parts of H are dealt so that an XCD sees few of
-// them: its share of the terms stays in its L2.  8192 x 7168 x 256: 95 us for 90
+// them: its share of the terms stays in its L2.  8192 x 7168 x 256: 92 us for 90
 // Gflop of products (a large library product runs at 1.37 Pflop/s here, 66 us);
 // loads alone 50 us, products and LDS reads 75.  Alternating the waves of a SIMD
 // between reading and multiplying, as the int8 linear layer does, took 105 us.
@@ -822,7 +822,7 @@ __device__ __forceinline__ void settle(const ScoredPass &p, int t, int wave, int
 // whole token and goes the same way: groups around the border are decided on fp64
 // values first, then the slots; without a bound, or with more than 64 slots,
 // every expert that may be among the k largest is summed again.  8192 tokens of
-// 256 experts leave about 520 open, some 80 of them for their groups.
+// 256 experts leave about 900 open, some 100 of them for their groups.
 template <int MAXPL>
 __global__ __launch_bounds__(64 * EXACT_WAVES) void scored_split_exact(ScoredPass p, int parts, float rounding)
 {

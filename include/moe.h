@@ -380,16 +380,21 @@ int moe_expert_cache_prefetch(moe_expert_cache *c, int layer_id, const moe_layer
  * 2^-24 (60 + hidden / 128) |x| |w_e|, in practice about 1e-7 of a logit's spread): a
  * token's weights depend on the batch it comes in to that, its experts only where
  * selection values agree to fp64's own roundings, as fp64 logits are summed in an
- * order that hangs on the batch's size (equal rows of w_router tie in all).  Where c = -inf (a bias of -inf, a group not kept, a NaN score,
- * which counts as p = 0 and c = -inf) an expert is chosen only if fewer than k
- * others are left, and then has weight 0; a token with nothing left gets k
- * weights of 0.  (A logit of +inf has sigmoid 1, and all of the softmax,
- * shared evenly among several.)
- * T < 2^22 (MOE_ERR_UNSUPPORTED otherwise).  R->n_experts = E <= 1024, top_k = k <= min(64, keep_groups * E / n_groups),
- * n_groups <= 64 divides E, hidden H a multiple of 8.  x: [T] rows of H elements of
- * type act, ldx elements apart; x, w_router ([E][H] fp32) and ws 16-byte
- * aligned, ldx a multiple of 8.  Workspace: moe_route_scored_workspace_bytes()
- * (0 if R is invalid); it serves every batch of up to T tokens. */
+ * order that hangs on the batch's size (equal rows of w_router tie in all).
+ * Where c = -inf (a bias of -inf, a group not kept, a NaN score, which counts as
+ * p = 0 and c = -inf) an expert is chosen only if fewer than k others are left, and
+ * then has weight 0; a token with nothing left gets k weights of 0.  (A logit of
+ * +inf has sigmoid 1, and all of the softmax, shared evenly among several.)
+ * Masks are best a bias of -inf: a finite one of large magnitude, -1e9 say, leaves
+ * a large batch's scores no room in fp32, and every token is decided on fp64 sums
+ * (8192 x 7168, 256 experts: 4 ms, and 0.16 ms with -inf); tokens of zeros, whose
+ * scores all tie, are too where there is no bias.
+ * T < 2^22 (MOE_ERR_UNSUPPORTED otherwise).  R->n_experts = E <= 1024, top_k = k <=
+ * min(64, keep_groups * E / n_groups), n_groups <= 64 divides E, hidden H a multiple
+ * of 8.  x: [T] rows of H elements of type act, ldx elements apart; x, w_router
+ * ([E][H] fp32) and ws 16-byte aligned, ldx a multiple of 8.  Workspace:
+ * moe_route_scored_workspace_bytes() (0 if R is invalid); it serves every batch of
+ * up to T tokens. */
 enum moe_score { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
 #define MOE_ROUTER_RENORM 1
 typedef struct moe_router {
@@ -423,7 +428,8 @@ size_t moe_route_scored_workspace_bytes(const moe_router *R, int T);
  *   elements); element-aligned pointers and strides run, 16-byte aligned rows
  *   of H % 8 == 0 run fastest.  1 <= hidden <= 65536.
  * moe_quant_i8: rows of x to int8.  With MOE_Q8_SWIGLU a row of x is [gate K |
- *   up K] and v = silu(gate) * up, silu(a) = a / (1 + exp(-a)) in fp32.
+ *   up K] and v = silu(gate) * up, silu(a) = a / (1 + exp(-a)) in fp32, off by at
+ *   most 7 half units in the last place with up's product; gates of any size.
  *   1 <= K <= 65536.  Weights are quantized by the same call, a row per output
  *   channel.
  * T < 2^22 for both (MOE_ERR_UNSUPPORTED otherwise: split the rows).
