@@ -80,6 +80,12 @@ class LinearC(ctypes.Structure):
                 ("w", ctypes.c_void_p), ("w_scale", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
 
 
+class BlockC(ctypes.Structure):
+    """struct moe_block."""
+    _fields_ = [("norm", ctypes.POINTER(NormC)), ("router", ctypes.POINTER(RouterC)), ("layer", ctypes.POINTER(Layer)),
+                ("gate_up", ctypes.POINTER(LinearC)), ("down", ctypes.POINTER(LinearC)), ("act_n", ctypes.c_int32)]
+
+
 class Profile(ctypes.Structure):
     """struct moe_profile: bracket launch number `kernel` with two hipEvents."""
     _fields_ = [("kernel", ctypes.c_int32), ("n_launches", ctypes.c_int32),
@@ -93,7 +99,8 @@ EXPORTS = ["moe_route", "moe_expert_ffn_decode", "moe_expert_ffn_prefill", "q2_p
            "q2_packed_bytes", "moe_workspace_bytes", "moe_status_str", "moe_last_error",
            "moe_expert_ffn_decode_noalloc", "moe_layer_decode", "moe_expert_cache_bytes", "moe_expert_cache_init",
            "moe_expert_cache_map", "moe_expert_cache_prefetch", "moe_route_scored", "moe_route_scored_workspace_bytes",
-           "moe_residual_norm", "moe_quant_i8", "moe_linear_i8", "moe_linear_i8_workspace_bytes"]
+           "moe_residual_norm", "moe_quant_i8", "moe_linear_i8", "moe_linear_i8_workspace_bytes",
+           "moe_block_decode", "moe_block_decode_workspace_bytes"]
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 # measurement kernels the benchmark uses (csrc/moe_probe.h; not part of the layer's ABI)
 PROBE_EXPORTS = ["moe_probe_stream_read", "moe_probe_mfma_loop"]
@@ -152,6 +159,11 @@ def lib():
     L.moe_linear_i8.restype = i32
     L.moe_linear_i8_workspace_bytes.argtypes = [wp, i32]
     L.moe_linear_i8_workspace_bytes.restype = sz
+    bp = ctypes.POINTER(BlockC)
+    L.moe_block_decode.argtypes = [bp, i32, vp, i32, i64, vp, i32, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, sz, vp, pp]
+    L.moe_block_decode.restype = i32
+    L.moe_block_decode_workspace_bytes.argtypes = [bp, i32]
+    L.moe_block_decode_workspace_bytes.restype = sz
     L.moe_probe_stream_read.argtypes = [vp, sz, i32, i32, vp, vp]
     L.moe_probe_stream_read.restype = i32
     L.moe_probe_mfma_loop.argtypes = [i32, i32, i32, vp, vp]
@@ -568,3 +580,53 @@ def route_scored(w: RouterWeights, x, r: Routing, ws, stream=None, prof=None):
                                             r.offsets.data_ptr(), r.perm.data_ptr(), r.inv.data_ptr(), ws.data_ptr(),
                                             ws.nbytes, _stream(stream), None if prof is None else ctypes.byref(prof)),
            "moe_route_scored")
+
+
+# ------------------------------------------------------------------ a block for a few tokens
+class BlockWeights:
+    """The weights of one MoE block: norm, router, a DeviceLayer without a shared expert (CB2 gate/up, Q2K down), and the
+    shared expert's LinearI8 of rows [gate | up] and down, or None for both.  act: the type (torch.bfloat16 or
+    torch.float32) that the norm's result is rounded to."""
+
+    def __init__(self, norm: NormWeights, router: RouterWeights, layer: DeviceLayer, gate_up: LinearI8 | None = None,
+                 down: LinearI8 | None = None, act=None):
+        import torch
+        self.parts = [norm, router, layer, gate_up, down]
+        self.hidden, self.n_experts, self.top_k = norm.hidden, router.n_experts, router.top_k
+        self.c = BlockC(*(None if part is None else ctypes.pointer(part.c) for part in self.parts),
+                        (_ACTS or _acts())[torch.bfloat16 if act is None else act])
+        self.ref = ctypes.byref(self.c)
+
+    def workspace(self, T: int, device="cuda"):
+        """A workspace for up to T tokens, for calls that do not overlap in time."""
+        import torch
+        n = int(lib().moe_block_decode_workspace_bytes(self.ref, T))
+        if n == 0:
+            raise ValueError("no workspace for %d tokens: %s" % (T, lib().moe_last_error().decode()))
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def block_decode(w: BlockWeights, x, residual, total, y, r: Routing, ws, stream=None, prof=None):
+    """s = x + residual (kept in `total`, which may be `residual`; both may be None), the routing of norm(s) into r, and the
+    experts' y (fp32) of up to 16 tokens (see moe_block_decode)."""
+    T, H = x.shape[0], w.hidden
+    ax, ldx = _rows(x, T, H, "x")
+    ay, ldy = _rows(y, T, H, "y")
+    ar = ldr = lds = 0
+    pr = pt = None
+    if residual is not None:
+        ar, ldr = _rows(residual, T, H, "residual")
+        pr = residual.data_ptr()
+    if total is not None:
+        at, lds = _rows(total, T, H, "total")
+        if pr is None or at != ar:
+            raise ValueError("total: needs a residual, and its type")
+        pt = total.data_ptr()
+    if ay != ACT_F32:
+        raise ValueError("y: fp32 is needed")
+    if r.topk_idx.shape != (T, w.top_k) or r.offsets.shape[0] != w.n_experts + 1:
+        raise ValueError("routing buffers of another shape")
+    _check((_lib or lib()).moe_block_decode(w.ref, T, x.data_ptr(), ax, ldx, pr, ar, ldr, pt, lds, y.data_ptr(), ldy,
+                                            r.topk_idx.data_ptr(), r.topk_w.data_ptr(), r.offsets.data_ptr(),
+                                            r.perm.data_ptr(), r.inv.data_ptr(), ws.data_ptr(), ws.nbytes, _stream(stream),
+                                            None if prof is None else ctypes.byref(prof)), "moe_block_decode")

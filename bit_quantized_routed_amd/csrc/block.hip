@@ -1,0 +1,893 @@
+// One MoE block for a few tokens in two kernels.
+//
+//   s = x + res;  n = rms_norm(s);  scored routing of n;
+//   y = sum_j w_j FFN_{e_j}(n) + FFN_shared(n)
+//
+// The first kernel is the norm.  The second does everything else: its work is cut
+// into items (a router row, 8 features of the shared gate/up, F features of a
+// routed expert's gate/up, some rows of y) that work-groups draw by ticket, in
+// that order, and an item waits only for items of lower tickets: for the
+// selection (made by the work-group that finishes the last router row), for h of
+// all experts.  Tickets are drawn by running work-groups only, so the lowest
+// unfinished item is always being worked on and every wait ends, however many
+// work-groups are resident and whatever else runs on the device.  (A bound on
+// the polls ends a wait all the same, should a second call overwrite the
+// workspace; y is NaN then.)
+//
+// Data that a work-group hands to others goes past its XCD's cache (agent-scope
+// stores; the arrival counter is raised after they are acknowledged).
+//
+// Arithmetic.  An activation block of 256 is x = scale * q with integers |q| <= 127
+// * 2^16 (23 bits and a sign below the block's largest value), written in three
+// int8 digits, so that dot products with integer weights run on the int8 matrix
+// instructions exactly: CB2's s_j C and Q2_K's sc_j q are at most 45, the shared
+// expert's weights are int8 as they are.  A block's sums leave as fp32, times its
+// scales, and are added in fp32.  The one rounding of the activations is 2^-24 of
+// their block's largest value, as fine as fp32's own for that value.
+//
+// A lane streams a quantized block of its own (a row's four consecutive blocks are
+// read by one load, lanes r + 16 g, g = 0..3); the matrix instruction's 16 rows are
+// four blocks x (three digits and a spare), zero where a lane's block is another
+// one: sums of different blocks never mix, and each arrives in the lane that holds
+// the block's scale.
+#include "block.h"
+#include "common.h"
+#include "devcache.h"
+#include "scored_dev.h"
+
+#include <algorithm>
+
+namespace moe {
+
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(4)));
+
+constexpr int NT = 1024, NW = NT / 64;
+constexpr int QUAD = 3072;                       // bytes of four blocks' digits: [16 steps][4 blocks][3 digits][16]
+constexpr float QMAX = 8323072.0f;               // 127 * 2^16
+constexpr int LINE = 32;                         // uint32s of a counter's line
+enum { C_TICKET = 0, C_ROUTER = LINE, C_LIST = 2 * LINE, C_SHARED = 3 * LINE, C_ROUTED = 4 * LINE, C_WORDS = 5 * LINE };
+constexpr int TABLE = 32768;                     // LDS: [256 codewords][16 copies][8 selectors]
+constexpr int O_ZERO = TABLE;                    // zeros for the lanes whose rows of the matrix instruction are empty
+constexpr int O_END = TABLE + QUAD;
+
+__device__ __forceinline__ float to_f32(const uint32_t w, int hi) { return __uint_as_float(hi ? w & 0xffff0000u : w << 16); }
+
+template <class T>
+__device__ __forceinline__ T peek(const T *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+template <class T>
+__device__ __forceinline__ void post(T *p, T v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+// three signed digits of base 256, least first
+__device__ __forceinline__ void digits(int q, int &d0, int &d1, int &d2)
+{
+    d0 = (int)(int8_t)q;
+    q = (q - d0) >> 8;
+    d1 = (int)(int8_t)q;
+    d2 = (q - d1) >> 8;
+}
+
+__device__ __forceinline__ uint32_t bytes4(int a, int b, int c, int d)
+{
+    return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
+}
+
+// scale and its reciprocal for a block whose largest magnitude has the bits m (an infinity or a NaN wins, and makes the scale NaN)
+__device__ __forceinline__ float block_scale(uint32_t m, float &inv)
+{
+    const float amax = __uint_as_float(m);
+    const bool finite = m < 0x7f800000u, some = amax >= 0x1p-100f;
+    inv = finite && some ? QMAX / amax : 0.0f;
+    return !finite ? __uint_as_float(0x7fc00000u) : some ? amax / QMAX : 0.0f;
+}
+
+// ---------------------------------------------------------------- norm
+// A work-group a token, 8 elements a thread: the operations of the row kernels'
+// norm, in their order; then the digits of n.  Clears the counters.
+__device__ __forceinline__ void load8(const void *p, int bf16, int64_t at, float v[8])
+{
+    if (bf16) {
+        const u32x4 u = *(const u32x4 *)((const uint16_t *)p + at);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = to_f32(u[j >> 1], j & 1);
+    } else {
+        const f32x4 a = *(const f32x4 *)((const float *)p + at), b = *(const f32x4 *)((const float *)p + at + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) { v[j] = a[j]; v[4 + j] = b[j]; }
+    }
+}
+
+__device__ __forceinline__ uint32_t bf16_bits(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+
+__global__ __launch_bounds__(NT) void block_norm(BlockPass p)
+{
+    __shared__ double part[NW];
+    const int tid = threadIdx.x, t = blockIdx.x, c = 8 * tid;
+    if (t == 0 && tid < C_WORDS) p.ctl[tid] = 0;
+    const bool in = c < p.H;
+    float v[8], g[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = g[j] = 0.0f;
+    if (in) {
+        load8(p.x, p.x_bf16, (int64_t)t * p.ldx + c, v);
+        load8(p.norm_w, 0, c, g);
+        if (p.res) {
+            float r[8];
+            load8(p.res, p.res_bf16, (int64_t)t * p.ldres + c, r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = v[j] + r[j];
+                if (p.res_bf16) v[j] = __uint_as_float(bf16_bits(v[j]) << 16);
+            }
+            if (p.sum) {
+                const int64_t at = (int64_t)t * p.ldsum + c;
+                if (p.res_bf16) {
+                    u32x4 u;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) u[j] = bf16_bits(v[2 * j]) | bf16_bits(v[2 * j + 1]) << 16;
+                    *(u32x4 *)((uint16_t *)p.sum + at) = u;
+                } else {
+                    *(f32x4 *)((float *)p.sum + at) = f32x4{v[0], v[1], v[2], v[3]};
+                    *(f32x4 *)((float *)p.sum + at + 4) = f32x4{v[4], v[5], v[6], v[7]};
+                }
+            }
+        }
+    }
+    double ss = 0.0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fma((double)v[j], (double)v[j], ss);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) ss += __shfl_xor(ss, off, 64);
+    if ((tid & 63) == 0) part[tid >> 6] = ss;
+    __syncthreads();
+    ss = part[0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) ss += part[w];
+    const float r = (float)(1.0 / sqrt(ss / (double)p.H + (double)p.eps));
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        v[j] = in ? (v[j] * r) * g[j] : 0.0f;
+        if (p.n_bf16) v[j] = __uint_as_float(bf16_bits(v[j]) << 16);
+        m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+    }
+    if (in) {
+        float *o = p.n + (int64_t)t * p.H + c;
+        *(f32x4 *)o = f32x4{v[0], v[1], v[2], v[3]};
+        *(f32x4 *)(o + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));  // the 32 threads of a block
+    if (c >= p.nq * 1024) return;
+    float inv;
+    const float scale = block_scale(m, inv);
+    if ((tid & 31) == 0) p.scales[t * 4 * p.nq + (tid >> 5)] = scale;
+    int d[8][3];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) digits((int)rintf(v[j] * inv), d[j][2], d[j][1], d[j][0]);
+    // block tid / 32, step tid / 2 % 16, half tid % 2
+    int8_t *o = p.planes + ((int64_t)t * p.nq + (tid >> 7)) * QUAD + ((tid >> 1) & 15) * 192 + ((tid >> 5) & 3) * 48 + (tid & 1) * 8;
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+        *(uint2 *)(o + 16 * q) = uint2{bytes4(d[0][q], d[1][q], d[2][q], d[3][q]), bytes4(d[4][q], d[5][q], d[6][q], d[7][q])};
+}
+
+// ---------------------------------------------------------------- the rest
+__device__ __forceinline__ i32x4 mfma_i8(const i32x4 &a, const i32x4 &b, const i32x4 &c)
+{
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+
+// the sum that three digits' sums (most significant first) stand for
+__device__ __forceinline__ float joined(const i32x4 &a) { return fmaf((float)a[0], 65536.0f, (float)(a[1] * 256 + a[2])); }
+
+extern __shared__ __align__(16) int8_t smem[];
+
+// Thread 0 waits until *p is at least n; false if that does not come (two seconds or more).
+constexpr int POLLS = 1 << 21;
+
+__device__ bool wait_for(const uint32_t *p, uint32_t n)
+{
+    for (int i = 0; i < POLLS; ++i) {
+        if (peek(p) >= n) return true;
+        __builtin_amdgcn_s_sleep(1);
+    }
+    return false;
+}
+
+// All of a work-group's posts are acknowledged before thread 0 raises the counter.
+__device__ __forceinline__ uint32_t arrive(uint32_t *p)
+{
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    uint32_t before = 0;
+    if (threadIdx.x == 0) before = __hip_atomic_fetch_add(p, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return before;
+}
+
+// digits and scales of tokens t0 .. t0 + n - 1 (list: of the tokens in it) into LDS slots
+__device__ void stage_tokens(const BlockPass &p, int t0, const int16_t *tokens, int n)
+{
+    const int per = p.nq * (QUAD / 16);
+    for (int i = threadIdx.x; i < n * per; i += NT) {
+        const int j = i / per, t = tokens ? tokens[j] : t0 + j;
+        ((u32x4 *)(smem + p.o_planes))[i] = ((const u32x4 *)p.planes)[(int64_t)t * per + (i - j * per)];
+    }
+    float *const sc = (float *)(smem + p.o_scales);
+    for (int i = threadIdx.x; i < n * 4 * p.nq; i += NT) {
+        const int j = i / (4 * p.nq), t = tokens ? tokens[j] : t0 + j;
+        sc[i] = p.scales[t * 4 * p.nq + (i - j * 4 * p.nq)];
+    }
+}
+
+// ---- a router row: fp64 logits of one expert
+__device__ void router_item(const BlockPass &p, int e)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = 8 * tid;
+    double *const part = (double *)(smem + p.o_red);                   // [NW][T]
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 0.0f;
+    const int at = min(c, p.H - 8);
+    if (c < p.H) load8(p.route.w, 0, (int64_t)e * p.H + c, w);
+    for (int t = 0; t < p.T; ++t) {
+        float v[8];
+        load8(p.n, 0, (int64_t)t * p.H + at, v);
+        double s = 0.0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = fma(c < p.H ? (double)v[j] : 0.0, (double)w[j], s);
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
+        if (lane == 0) part[wave * BLOCK_MAX_T + t] = s;
+    }
+    __syncthreads();
+    if (tid < p.T) {
+        double s = part[tid];
+        for (int v = 1; v < NW; ++v) s += part[v * BLOCK_MAX_T + tid];
+        post(p.logits + (int64_t)tid * p.E + e, s);
+    }
+}
+
+// ---- the selection: a wave a token, then the grouping and the list of experts
+template <int MAXPL>
+__device__ void select(const BlockPass &p)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int E = p.E, k = p.k, n = p.T * k;
+    __shared__ int16_t chosen[BLOCK_MAX_T * BLOCK_MAX_K];
+    __shared__ float weight[BLOCK_MAX_T * BLOCK_MAX_K];
+    __shared__ uint32_t mask[BLOCK_MAX_E];       // tokens of an expert
+    __shared__ int16_t first[BLOCK_MAX_E];
+    __shared__ int sums[2][NW];
+    double *const cs = (double *)(smem + p.o_planes);                  // [T][E]
+    if (tid < BLOCK_MAX_E) mask[tid] = 0;
+    if (wave < p.T) {
+        double l[MAXPL], pr[MAXPL], c[MAXPL];
+#pragma unroll
+        for (int i = 0; i < MAXPL; ++i)
+            l[i] = lane + 64 * i < E ? peek(p.logits + (int64_t)wave * E + lane + 64 * i) : -INFINITY;
+        token_scores<MAXPL>(p.route, l, lane, pr, c);
+        if (p.route.keep < p.route.groups) {
+            const Groups<double> g = rank_groups<MAXPL, double>(p.route, lane, c, cs + wave * E);
+            const float inv = 1.0f / (float)(E / p.route.groups);
+#pragma unroll
+            for (int i = 0; i < MAXPL; ++i)
+                if (!(g.kept >> group_of(min(lane + 64 * i, E - 1), inv) & 1)) c[i] = -INFINITY;
+        }
+        int my_e;
+        double my_c, my_p;
+        uint32_t taken;
+        select64<MAXPL>(p.route, lane, c, pr, my_e, my_c, my_p, taken);
+        const float w = write_token(p.route, wave, lane, my_e, lane < k && my_c != -INFINITY ? my_p : 0.0);
+        if (lane < k) {
+            chosen[wave * k + lane] = (int16_t)my_e;
+            weight[wave * k + lane] = w;
+        }
+    }
+    __syncthreads();
+    if (tid < n) atomicOr(&mask[chosen[tid]], 1u << (tid / k));
+    __syncthreads();
+    // positions and numbers of the experts, by an inclusive sum over waves and then their totals
+    const uint32_t m = tid < E ? mask[tid] : 0;
+    int upto = __popc(m), used = m != 0;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int a = __shfl_up(upto, off, 64), b = __shfl_up(used, off, 64);
+        if (lane >= off) { upto += a; used += b; }
+    }
+    if (lane == 63) { sums[0][wave] = upto; sums[1][wave] = used; }
+    __syncthreads();
+    int all = 0;
+    for (int w = 0; w < NW; ++w) {
+        if (w < wave) { upto += sums[0][w]; used += sums[1][w]; }
+        all += sums[1][w];
+    }
+    const int begin = upto - __popc(m);
+    if (tid < E) {
+        first[tid] = (int16_t)begin;
+        p.route.offsets[tid] = begin;
+        if (m) post(p.list + used - 1, (int32_t)(tid | begin << 10 | (int)__popc(m) << 20));
+    }
+    if (tid == 0) p.route.offsets[E] = n;
+    __syncthreads();
+    if (tid < n) {
+        const int t = tid / k, e = chosen[tid], pos = first[e] + __popc(mask[e] & ((1u << t) - 1u));
+        p.route.perm[pos] = tid;
+        p.route.inv[tid] = pos;
+        post(p.list + 256 + pos, t);
+        post((float *)p.list + 512 + pos, weight[tid]);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid == 0) post(p.ctl + C_LIST, (uint32_t)all);
+}
+
+// ---- 8 features of the shared gate/up: a tile of rows gate f .. f + 7, up f .. f + 7; a wave's blocks of K are wave, wave + 16, ..
+__device__ __forceinline__ const int8_t *digit_base(const BlockPass &p, bool in, int slot, int stride, int at)
+{
+    return in ? smem + p.o_planes + slot * stride + at : smem + O_ZERO;
+}
+
+__device__ __forceinline__ i32x4 load_row16(const int8_t *row, int at, int K)
+{
+    i32x4 v = {0, 0, 0, 0};
+    if (at < K) v = *(const i32x4 *)(row + at);
+    return v;
+}
+
+__device__ void shared_item(const BlockPass &p, int item, int t0, int nt)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    const int f = 8 * item + (r & 7);
+    const int8_t *const row = p.sh_up + (int64_t)((r < 8 ? 0 : p.sh) + min(f, p.sh - 1)) * p.ld_up;
+    const int slot = r >> 2, digit = r & 3;                            // this lane's row of the instruction
+    const bool in = digit < 3 && slot < nt;
+    const float *const sc = (const float *)(smem + p.o_scales) + min(g, nt - 1) * 4 * p.nq;
+    float v = 0.0f;
+    for (int b = wave; b < p.nb; b += NW) {
+        i32x4 w[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) w[s] = load_row16(row, 256 * b + 64 * s + 16 * g, p.H);
+        const int8_t *const a = digit_base(p, in, slot, p.nq * QUAD, (b >> 2) * QUAD + g * 192 + ((b & 3) * 3 + digit) * 16);
+        i32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) acc = mfma_i8(*(const i32x4 *)(a + s * 768), w[s], acc);
+        v = fmaf(joined(acc), sc[b], v);                               // lane (r, g): row r, token g
+    }
+    float *const red = (float *)(smem + p.o_red);
+    red[wave * 64 + lane] = v;
+    __syncthreads();
+    if (tid < 32 && (tid >> 3) < nt && 8 * item + (tid & 7) < p.sh) {
+        const int fo = tid & 7, t = tid >> 3, ff = 8 * item + fo;
+        float a = 0.0f, u = 0.0f;
+        for (int w = 0; w < NW; ++w) {
+            a += red[w * 64 + 16 * t + fo];
+            u += red[w * 64 + 16 * t + 8 + fo];
+        }
+        a *= p.up_scale[ff];
+        u *= p.up_scale[p.sh + ff];
+        if (p.up_bias) { a += p.up_bias[ff]; u += p.up_bias[p.sh + ff]; }
+        post(p.hs + (int64_t)(t0 + t) * p.sh + ff, a / (1.0f + expf(-a)) * u);
+    }
+}
+
+// ---- F features of a routed expert's gate/up, N tokens (their digits in slots s0 ..): a unit is 16 features and a quad of blocks
+struct Window { uint32_t w[10]; };
+
+__device__ __forceinline__ Window load_window(const uint8_t *at)
+{
+    const uint32_t *const q = (const uint32_t *)((uintptr_t)at & ~(uintptr_t)3);
+    const u32x4u a = *(const u32x4u *)q, b = *(const u32x4u *)(q + 4);
+    const u32x2u c = *(const u32x2u *)(q + 8);
+    return Window{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3], c[0], c[1]}};
+}
+
+// Fields of a block whose first byte is byte 0 (odd = 0) or 2 of its window.
+struct Cb2 {
+    uint32_t idx[8], scales;
+    float d;
+    __device__ __forceinline__ Cb2(const Window &v, bool odd)
+    {
+        const uint32_t sel = odd ? 0x07060504u : 0x05040302u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) idx[j] = __builtin_amdgcn_perm(v.w[2 + j], v.w[1 + j], sel);
+        scales = __builtin_amdgcn_perm(v.w[1], v.w[0], sel);
+        d = f16_bits_to_f32((odd ? v.w[0] >> 16 : v.w[0]) & 0xffffu);
+    }
+    // the bytes -3 s, -s, s, 3 s of sub-block j: 0x80 - b, its top bit flipped, is -b without a borrow into the next byte
+    __device__ __forceinline__ uint32_t pool(int j) const
+    {
+        const uint32_t s = (scales >> (4 * j)) & 15u;
+        return ((0x8080u - s * 0x0103u) ^ 0x8080u) | s * 0x0301u << 16;
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void routed_unit(const BlockPass &p, const Window &gw, const Window &uw, bool godd, bool uodd,
+                                            const int8_t *const a[N], i32x4 ag[N], i32x4 au[N], float &dg, float &du)
+{
+    const Cb2 gb(gw, godd), ub(uw, uodd);
+    const uint32_t copy = (threadIdx.x & 15) * 8;
+    auto code = [&](uint32_t idx, int b) {
+        const uint32_t at = ((b == 0 ? idx << 7 : idx >> (8 * b - 7)) & 0x7f80u) | copy;
+        return *(const uint2 *)(smem + at);
+    };
+#pragma unroll
+    for (int n = 0; n < N; ++n) ag[n] = au[n] = i32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t gp = gb.pool(j), upool = ub.pool(j);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            i32x4 w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint2 x = code(gb.idx[j], 2 * q + i), y = code(ub.idx[j], 2 * q + i);
+                w[0][2 * i] = (int)__builtin_amdgcn_perm(gp, gp, x.x);
+                w[0][2 * i + 1] = (int)__builtin_amdgcn_perm(gp, gp, x.y);
+                w[1][2 * i] = (int)__builtin_amdgcn_perm(upool, upool, y.x);
+                w[1][2 * i + 1] = (int)__builtin_amdgcn_perm(upool, upool, y.y);
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const i32x4 x = *(const i32x4 *)(a[n] + (2 * j + q) * 192);
+                ag[n] = mfma_i8(x, w[0], ag[n]);
+                au[n] = mfma_i8(x, w[1], au[n]);
+            }
+        }
+    }
+    dg = gb.d;
+    du = ub.d;
+}
+
+template <int N>
+__device__ void routed_units(const BlockPass &p, int e, int f0, int n, const int16_t *slots)
+{
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+    const int units = p.F / 16 * p.nq;
+    const bool in = (r & 3) < 3 && (r >> 2) == g;
+    const float *const sc = (const float *)(smem + p.o_scales);
+    float *const red = (float *)(smem + p.o_red);                      // [units][N][gate, up][16]
+    auto block_at = [&](const uint8_t *w, int u) {
+        const int row = min(f0 + u / p.nq * 16 + r, p.I - 1), b = min(4 * (u % p.nq) + g, p.nb - 1);
+        return w + (((int64_t)e * p.I + row) * p.nb + b) * 38;
+    };
+    Window gw, uw;
+    if (wave < units) {
+        gw = load_window(block_at(p.gate, wave));
+        uw = load_window(block_at(p.up, wave));
+    }
+    for (int u = wave; u < units; u += NW) {
+        const Window g0 = gw, u0 = uw;
+        const bool godd = (uintptr_t)block_at(p.gate, u) & 2, uodd = (uintptr_t)block_at(p.up, u) & 2;
+        if (u + NW < units) {
+            gw = load_window(block_at(p.gate, u + NW));
+            uw = load_window(block_at(p.up, u + NW));
+        }
+        const int q = u % p.nq, b = 4 * q + g;
+        const int8_t *a[N];
+        i32x4 ag[N], au[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            a[j] = digit_base(p, in && j < n, slots[min(j, n - 1)], p.nq * QUAD, q * QUAD + ((r >> 2) * 3 + (r & 3)) * 16);
+        float dg, du;
+        routed_unit<N>(p, g0, u0, godd, uodd, a, ag, au, dg, du);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float s = b < p.nb && j < n ? sc[slots[min(j, n - 1)] * 4 * p.nq + b] : 0.0f;
+            float x = b < p.nb ? joined(ag[j]) * (dg * s) : 0.0f, y = b < p.nb ? joined(au[j]) * (du * s) : 0.0f;
+            x += __shfl_xor(x, 16, 64);
+            y += __shfl_xor(y, 16, 64);
+            x += __shfl_xor(x, 32, 64);
+            y += __shfl_xor(y, 32, 64);
+            if (g < 2) red[(u * N + j) * 32 + lane] = g ? y : x;
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n * p.F; i += NT) {
+        const int j = i / p.F, f = i % p.F;
+        float a = 0.0f, u = 0.0f;
+        for (int q = 0; q < p.nq; ++q) {
+            const float *const x = red + ((f / 16 * p.nq + q) * N + j) * 32 + f % 16;
+            a += x[0];
+            u += x[16];
+        }
+        // row of h: the position, which slots[] is followed by
+        if (f0 + f < p.I) post(p.h + (int64_t)slots[BLOCK_MAX_T + j] * p.Ip + f0 + f, a / (1.0f + expf(-a)) * u);
+    }
+}
+
+__device__ void routed_item(const BlockPass &p, int item, bool &resident)
+{
+    __shared__ int16_t tokens[2 * BLOCK_MAX_T], slots[2 * BLOCK_MAX_T];
+    const int d = item / p.nf, f0 = item % p.nf * p.F;
+    const int entry = peek(p.list + d), e = entry & 1023, first = entry >> 10 & 1023, n = entry >> 20;
+    for (int j0 = 0; j0 < n; j0 += 4) {
+        const int m = min(4, n - j0);
+        __syncthreads();
+        if (threadIdx.x < m) {
+            tokens[threadIdx.x] = (int16_t)peek(p.list + 256 + first + j0 + threadIdx.x);
+            slots[threadIdx.x] = p.T <= p.slots ? tokens[threadIdx.x] : (int16_t)threadIdx.x;
+            slots[BLOCK_MAX_T + threadIdx.x] = (int16_t)(first + j0 + threadIdx.x);
+        }
+        __syncthreads();
+        if (p.T > p.slots) {
+            stage_tokens(p, 0, tokens, m);
+            resident = false;
+            __syncthreads();
+        }
+        if (m == 1) routed_units<1>(p, e, f0, m, slots);
+        else if (m == 2) routed_units<2>(p, e, f0, m, slots);
+        else routed_units<4>(p, e, f0, m, slots);
+    }
+}
+
+// ---- some rows of y: the shared expert's down rows and every chosen expert's
+// Digits of rows of h into LDS: row i (of `count`) is at src + i * ld, n elements; natural order, or for Q2_K dword j of a step =
+// weights j, j + 4, j + 8, j + 12, with the sums of its 16 sub-blocks in four digits.
+template <bool Q2K>
+__device__ void stage_h(const BlockPass &p, const float *src, int64_t ld, int count, int n, int nq)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, grp = lane >> 2, j = lane & 3;
+    const int nb = 4 * nq;
+    int8_t *const planes = smem + p.o_planes, *const sums = planes + count * nq * QUAD;
+    float *const sc = (float *)(sums + (Q2K ? count * nb * 64 : 0));
+    constexpr int B = 4;
+    for (int i0 = wave; i0 < count * nb; i0 += B * NW) {
+        float v[B][4];
+#pragma unroll
+        for (int q = 0; q < B; ++q) {
+            const int i = i0 + q * NW, row = i / nb, f = 256 * (i - row * nb) + 16 * grp + (Q2K ? j : 4 * j);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int at = f + (Q2K ? 4 * c : c);
+                v[q][c] = i < count * nb && at < n ? peek(src + row * ld + at) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < B; ++q) {
+            const int i = i0 + q * NW;
+            if (i >= count * nb) break;
+            const int row = i / nb, b = i - row * nb;
+            uint32_t m = 0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) m = max(m, __float_as_uint(v[q][c]) & 0x7fffffffu);
+#pragma unroll
+            for (int off = 32; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
+            float inv;
+            const float scale = block_scale(m, inv);
+            int x[4], d[4][3];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                x[c] = (int)rintf(v[q][c] * inv);
+                digits(x[c], d[c][2], d[c][1], d[c][0]);
+            }
+            int8_t *const o = planes + (row * nq + (b >> 2)) * QUAD + grp * 192 + (b & 3) * 48 + 4 * j;
+#pragma unroll
+            for (int c = 0; c < 3; ++c) *(uint32_t *)(o + 16 * c) = bytes4(d[0][c], d[1][c], d[2][c], d[3][c]);
+            if (Q2K) {
+                int s = x[0] + x[1] + x[2] + x[3];
+                s += __shfl_xor(s, 1, 64);
+                s += __shfl_xor(s, 2, 64);
+                int d0, d1, d2, d3 = (int)(int8_t)s;
+                digits((s - d3) >> 8, d2, d1, d0);
+                sums[(row * nb + b) * 64 + 16 * j + grp] = (int8_t)(j == 0 ? d0 : j == 1 ? d1 : j == 2 ? d2 : d3);
+            }
+            if (lane == 0) sc[row * nb + b] = scale;
+        }
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void down_unit(const uint32_t c[21], const int8_t *const a[N], const int8_t *const m[N], i32x4 acc[N],
+                                          i32x4 min_acc[N])
+{
+#pragma unroll
+    for (int n = 0; n < N; ++n) acc[n] = i32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < 16; ++s) {
+        const uint32_t sc = (c[1 + s / 4] >> (8 * (s & 3))) & 15u, q = c[5 + s];
+        const uint32_t pool = sc * 0x020100u | sc * 3u << 24;
+        i32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = (int)__builtin_amdgcn_perm(pool, pool, q >> (2 * i) & 0x03030303u);
+#pragma unroll
+        for (int n = 0; n < N; ++n) acc[n] = mfma_i8(*(const i32x4 *)(a[n] + s * 192), w, acc[n]);
+    }
+    i32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = (int)(c[1 + i] >> 4 & 0x0f0f0f0fu);
+#pragma unroll
+    for (int n = 0; n < N; ++n) min_acc[n] = mfma_i8(*(const i32x4 *)m[n], w, i32x4{0, 0, 0, 0});
+}
+
+// N rows of h from i0 on (LDS rows) with 16 rows of one expert's down matrix and a quad of its blocks, times the rows' weights,
+// onto this wave's sums
+template <int N>
+__device__ void down_rows(const BlockPass &p, const uint32_t c[21], int count, int i0, int n, int quad, const int32_t *tok,
+                          const float *weight, float *ya)
+{
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, nb = 4 * p.nqi, b = 4 * quad + g;
+    const int8_t *const planes = smem + p.o_planes, *const sums = planes + count * p.nqi * QUAD;
+    const float *const sc = (const float *)(sums + count * nb * 64);
+    const int beta = r >> 2, digit = r & 3;
+    const int8_t *a[N], *m[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int row = i0 + min(j, n - 1);
+        const bool in = beta == g && j < n;
+        a[j] = in && digit < 3 ? planes + (row * p.nqi + quad) * QUAD + (beta * 3 + digit) * 16 : smem + O_ZERO;
+        m[j] = in ? sums + (row * nb + b) * 64 + 16 * digit : smem + O_ZERO;
+    }
+    i32x4 acc[N], mins[N];
+    down_unit<N>(c, a, m, acc, mins);
+    const float d = f16_bits_to_f32(c[0] & 0xffffu), dmin = f16_bits_to_f32(c[0] >> 16);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        float v = 0.0f;
+        if (b < p.nbi && j < n) {
+            const float s = sc[(i0 + j) * nb + b];
+            const float off = fmaf((float)(mins[j][0] * 256 + mins[j][1]), 65536.0f, (float)(mins[j][2] * 256 + mins[j][3]));
+            v = joined(acc[j]) * (d * s) - off * (dmin * s);
+        }
+        v += __shfl_xor(v, 16, 64);
+        v += __shfl_xor(v, 32, 64);
+        if (g == 0 && j < n) ya[tok[i0 + j] * 32 + r] += weight[i0 + j] * v;
+    }
+}
+
+__device__ bool down_item(const BlockPass &p, int item, int n_list)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
+    __shared__ int32_t tok[BLOCK_MAX_T * BLOCK_MAX_K], entry[BLOCK_MAX_T * BLOCK_MAX_K];
+    __shared__ float weight[BLOCK_MAX_T * BLOCK_MAX_K];
+    __shared__ int ok;
+    const int r0 = item * p.rows, tiles = (p.rows + 15) / 16, n = p.T * p.k;
+    float *const ya_all = (float *)(smem + p.o_red), *const ya = ya_all + wave * p.T * 32;     // [NW][T][32]
+    __syncthreads();
+    for (int i = lane; i < p.T * 32; i += 64) ya[i] = 0.0f;
+    if (tid < n_list) entry[tid] = peek(p.list + tid);
+    if (tid < n) {
+        tok[tid] = peek(p.list + 256 + tid);
+        weight[tid] = peek((const float *)p.list + 512 + tid);
+    }
+    if (p.sh) {
+        if (tid == 0) ok = wait_for(p.ctl + C_SHARED, (uint32_t)p.t_shared);
+        __syncthreads();
+        if (!ok) return false;
+        const int rows_max = min(p.chunk, p.T), parts = (p.nbs + 1) / 2;
+        for (int t0 = 0; t0 < p.T; t0 += rows_max) {
+            const int nt = min(rows_max, p.T - t0);
+            __syncthreads();
+            stage_h<false>(p, p.hs + (int64_t)t0 * p.sh, p.sh, nt, p.sh, p.nqs);
+            __syncthreads();
+            const float *const sc = (const float *)(smem + p.o_planes + nt * p.nqs * QUAD);
+            for (int u = wave; u < tiles * parts; u += NW) {
+                const int tile = u % tiles, part = u / tiles;
+                const int row = min(r0 + tile * 16 + r, p.H - 1);
+                const int8_t *const wr = p.sh_down + (int64_t)row * p.ld_down;
+                const float ws = p.down_scale[row];
+                i32x4 w[2][4];
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) w[q][s] = load_row16(wr, 512 * part + 256 * q + 64 * s + 16 * g, p.sh);
+                for (int tg = 0; tg < nt; tg += 4) {
+                    const int slot = tg + (r >> 2), digit = r & 3, tt = tg + g;
+                    float v = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int b = 2 * part + q;
+                        const bool in = digit < 3 && slot < nt && b < 4 * p.nqs;
+                        const int8_t *const a =
+                            digit_base(p, in, slot, p.nqs * QUAD, (b >> 2) * QUAD + g * 192 + ((b & 3) * 3 + digit) * 16);
+                        i32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) acc = mfma_i8(*(const i32x4 *)(a + s * 768), w[q][s], acc);
+                        if (tt < nt && b < 4 * p.nqs) v = fmaf(joined(acc), sc[tt * 4 * p.nqs + b], v);
+                    }
+                    if (tt < nt) ya[(t0 + tt) * 32 + tile * 16 + r] += v * ws;
+                }
+            }
+        }
+    }
+    if (tid == 0) ok = wait_for(p.ctl + C_ROUTED, (uint32_t)(n_list * p.nf));
+    __syncthreads();
+    if (!ok) return false;
+    for (int c0 = 0; c0 < n; c0 += p.chunk) {
+        const int count = min(p.chunk, n - c0);
+        __syncthreads();
+        stage_h<true>(p, p.h + (int64_t)c0 * p.Ip, p.Ip, count, p.I, p.nqi);
+        __syncthreads();
+        // units (expert, quad of blocks, tile) dealt to the waves in turn
+        int unit = 0;
+        for (int d = 0; d < n_list; ++d) {
+            const int e = entry[d] & 1023, first = entry[d] >> 10 & 1023;
+            const int lo = max(first, c0), hi = min(first + (entry[d] >> 20), c0 + count);
+            if (lo >= hi) continue;
+            const int units = p.nqi * tiles;
+            for (int u = (wave - unit % NW + NW) % NW; u < units; u += NW) {
+                const int tile = u % tiles, quad = u / tiles;
+                const int row = min(r0 + tile * 16 + r, p.H - 1), b = min(4 * quad + g, p.nbi - 1);
+                const uint32_t *const at = (const uint32_t *)(p.down + (((int64_t)e * p.H + row) * p.nbi + b) * 84);
+                uint32_t c[21];
+#pragma unroll
+                for (int i = 0; i < 5; ++i) {
+                    const u32x4u v = *(const u32x4u *)(at + 4 * i);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) c[4 * i + q] = v[q];
+                }
+                c[20] = at[20];
+                for (int j = lo; j < hi; j += 4) {
+                    const int m = min(4, hi - j);
+                    const int32_t *const tk = tok + c0;
+                    const float *const wt = weight + c0;
+                    if (m == 1) down_rows<1>(p, c, count, j - c0, m, quad, tk, wt, ya + tile * 16);
+                    else if (m == 2) down_rows<2>(p, c, count, j - c0, m, quad, tk, wt, ya + tile * 16);
+                    else down_rows<4>(p, c, count, j - c0, m, quad, tk, wt, ya + tile * 16);
+                }
+            }
+            unit += units;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < p.T * p.rows; i += NT) {
+        const int t = i / p.rows, row = i % p.rows;
+        if (r0 + row >= p.H) continue;
+        float v = ya_all[t * 32 + row];
+        for (int w = 1; w < NW; ++w) v += ya_all[(w * p.T + t) * 32 + row];
+        if (p.sh && p.down_bias) v += p.down_bias[r0 + row];
+        p.y[(int64_t)t * p.ldy + r0 + row] = v;
+    }
+    return true;
+}
+
+template <int MAXPL>
+__global__ __launch_bounds__(NT) void block_kernel(BlockPass p)
+{
+    __shared__ uint32_t next, word;
+    const int tid = threadIdx.x;
+    // selectors of the codewords, 16 copies (a lane reads copy lane % 16: no two of 16 lanes share a bank)
+    for (int i = tid; i < 4096; i += NT) {
+        const uint2 c = *(const uint2 *)(p.codebook + 8 * (i >> 4));
+        // (C + 3) / 2 of bytes -3, -1, 1, 3, added without a carry into the next byte
+        auto code = [](uint32_t v) { return (((v & 0x7f7f7f7fu) + 0x03030303u) ^ (v & 0x80808080u)) >> 1 & 0x03030303u; };
+        *(uint2 *)(smem + 8 * i) = uint2{code(c.x), code(c.y)};
+    }
+    for (int i = tid; i < QUAD / 4; i += NT) ((uint32_t *)(smem + O_ZERO))[i] = 0;
+    uint32_t ticket = 0;
+    if (tid == 0) next = __hip_atomic_fetch_add(p.ctl + C_TICKET, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    bool resident = false, ok = true;
+    int n_list = -1;
+    for (;;) {
+        __syncthreads();
+        ticket = next;
+        __syncthreads();
+        uint32_t after = 0;
+        if (tid == 0) after = __hip_atomic_fetch_add(p.ctl + C_TICKET, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        int item = (int)ticket;
+        if (item < p.t_router) {
+            router_item(p, item);
+            if (tid == 0) word = 0;
+            const uint32_t before = arrive(p.ctl + C_ROUTER);
+            if (tid == 0) word = before + 1 == (uint32_t)p.t_router;
+            __syncthreads();
+            if (word) {
+                select<MAXPL>(p);
+                resident = false;
+            }
+        } else if ((item -= p.t_router) < p.t_shared) {
+            for (int t0 = 0; t0 < p.T; t0 += p.slots) {
+                if (!resident) {
+                    __syncthreads();
+                    stage_tokens(p, t0, nullptr, min(p.slots, p.T - t0));
+                    resident = p.T <= p.slots;
+                    __syncthreads();
+                }
+                shared_item(p, item, t0, min(p.slots, p.T - t0));
+            }
+            arrive(p.ctl + C_SHARED);
+        } else {
+            item -= p.t_shared;
+            if (n_list < 0) {
+                if (tid == 0) word = wait_for(p.ctl + C_LIST, 1) ? peek(p.ctl + C_LIST) : 0;
+                __syncthreads();
+                n_list = (int)word;
+                ok = n_list > 0;
+            }
+            if (ok && item < n_list * p.nf) {
+                if (!resident && p.T <= p.slots) {
+                    stage_tokens(p, 0, nullptr, p.T);
+                    resident = true;
+                }
+                routed_item(p, item, resident);
+                arrive(p.ctl + C_ROUTED);
+            } else if (ok && (item -= n_list * p.nf) < p.t_down) ok = down_item(p, item, n_list);
+            else if (ok) return;
+            if (!ok) {
+                for (int i = tid; i < p.T * p.H; i += NT) p.y[(int64_t)(i / p.H) * p.ldy + i % p.H] = __uint_as_float(0x7fc00000u);
+                return;
+            }
+        }
+        if (tid == 0) next = after;
+    }
+}
+
+}  // namespace
+
+void block_layout(BlockPass &p)
+{
+    auto up = [](int v, int to) { return (v + to - 1) / to; };
+    p.nb = up(p.H, 256); p.nq = up(p.nb, 4);
+    p.nbi = up(p.I, 256); p.nqi = up(p.nbi, 4);
+    p.nbs = up(p.sh, 256); p.nqs = up(p.nbs, 4);
+    p.Ip = up(p.I, 32) * 32;
+    p.F = p.nq >= 4 ? 64 : 128;
+    p.nf = up(p.I, p.F);
+    const int cus = cu_count();
+    p.rows = std::min(32, std::max(16, up(p.H, cus)));
+    p.t_router = p.E;
+    p.t_shared = up(p.sh, 8);
+    p.t_down = up(p.H, p.rows);
+    p.slots = std::min(p.T, 4);
+    // LDS: table, zeros, planes (or rows of h), scales, sums
+    const int units = p.F / 16 * p.nq;
+    const int red = std::max({units * (p.slots <= 2 ? p.slots : 4) * 128, NW * 64 * 4, NW * BLOCK_MAX_T * 8, NW * p.T * 128});
+    const int scales = p.slots * 4 * p.nq * 4;
+    const int row_i = p.nqi * (QUAD + 4 * 64 + 16), row_s = p.nqs * (QUAD + 16), row = std::max(row_i, row_s);
+    constexpr int LDS = 160 * 1024 - 8192;       // the static shared memory is apart
+    const int want = std::max({p.slots * p.nq * QUAD + scales, std::min(16, p.T * p.k) * row, p.T * p.E * 8});
+    const int room = LDS - O_END - red;
+    const int area = std::min(want, room) / 16 * 16;
+    p.chunk = std::min(area / row, p.T * p.k);
+    p.o_planes = O_END;
+    p.o_scales = O_END + p.slots * p.nq * QUAD;
+    p.o_red = O_END + area;
+    p.lds = O_END + area + red;
+}
+
+size_t block_workspace(BlockPass &p, char *base)
+{
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        char *at = base + off;
+        off = (off + bytes + 255) / 256 * 256;
+        return (void *)at;
+    };
+    p.ctl = (uint32_t *)take(C_WORDS * 4);
+    p.list = (int32_t *)take(768 * 4);
+    p.logits = (double *)take((size_t)p.T * p.E * 8);
+    p.n = (float *)take((size_t)p.T * p.H * 4);
+    p.planes = (int8_t *)take((size_t)p.T * p.nq * QUAD);
+    p.scales = (float *)take((size_t)p.T * 4 * p.nq * 4);
+    p.h = (float *)take((size_t)p.T * p.k * p.Ip * 4);
+    p.hs = (float *)take((size_t)p.T * p.sh * 4);
+    return off;
+}
+
+hipError_t launch_block_norm(const BlockPass &p, hipStream_t s)
+{
+    block_norm<<<p.T, NT, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+hipError_t launch_block(const BlockPass &p, hipStream_t s)
+{
+    const unsigned grid = (unsigned)cu_count();  // one work-group's LDS fills a CU
+#define MOE_BLOCK(pl)                                                                             \
+    do {                                                                                          \
+        static DevSlots slots{};                                                                  \
+        const hipError_t e = lds_limit((const void *)block_kernel<pl>, slots, p.lds);             \
+        if (e != hipSuccess) return e;                                                            \
+        block_kernel<pl><<<grid, NT, p.lds, s>>>(p);                                              \
+    } while (0)
+    if (p.E <= 256) MOE_BLOCK(4);
+    else MOE_BLOCK(8);
+#undef MOE_BLOCK
+    return hipGetLastError();
+}
+
+}  // namespace moe

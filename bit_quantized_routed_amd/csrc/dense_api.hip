@@ -3,78 +3,18 @@
 // validation and the launch sequences.
 #include <hip/hip_runtime.h>
 
+#include "block.h"
+#include "dense_check.h"
 #include "linear.h"
-#include "moe.h"
 #include "route.h"
-#include "rows.h"
 #include "scored.h"
-#include "status.h"
 
 using namespace moe;
 
 namespace {
 
 constexpr size_t ALIGN = 256;
-constexpr int MAX_ROWS = 1 << 22;                // rows of a call, up to 1024 threads each in a launch of fewer than 2^32
 size_t align_up(size_t v) { return (v + ALIGN - 1) / ALIGN * ALIGN; }
-
-int hip_fail(hipError_t e, const char *what) { return set_error(MOE_ERR_HIP, "%s: %s", what, hipGetErrorString(e)); }
-
-// Runs one launch of a call, between the caller's events if it is the profiled one.
-struct Launcher {
-    moe_profile *p;
-    hipStream_t s;
-    int n = 0;
-    template <class F>
-    int operator()(const char *name, F launch)
-    {
-        const bool timed = p && p->kernel == n;
-        if (timed) {
-            p->name = name;
-            const hipError_t e = hipEventRecord((hipEvent_t)p->ev_start, s);
-            if (e != hipSuccess) return hip_fail(e, "event record");
-        }
-        hipError_t e = launch();
-        if (e != hipSuccess) return hip_fail(e, name);
-        if (timed && (e = hipEventRecord((hipEvent_t)p->ev_stop, s)) != hipSuccess) return hip_fail(e, "event record");
-        ++n;
-        if (p) p->n_launches = n;
-        return MOE_OK;
-    }
-};
-
-bool act_ok(int a) { return a == MOE_ACT_F32 || a == MOE_ACT_BF16; }
-int act_size(int a) { return a == MOE_ACT_F32 ? 4 : 2; }
-
-// rows of T x n elements of `size` bytes, ld apart, starting at p
-int check_rows(const char *name, const void *p, int64_t ld, int T, int n, int size)
-{
-    if (!p) return set_error(MOE_ERR_INVALID_ARG, "%s is NULL", name);
-    if ((uintptr_t)p % size) return set_error(MOE_ERR_INVALID_ARG, "%s is not aligned to its elements", name);
-    if (ld < n && T > 1) return set_error(MOE_ERR_INVALID_ARG, "%s: rows of %d elements only %lld apart", name, n, (long long)ld);
-    if (ld < 0 || ld > ((int64_t)1 << 40)) return set_error(MOE_ERR_INVALID_ARG, "%s: stride %lld", name, (long long)ld);
-    return MOE_OK;
-}
-
-int check_scored(const moe_router *R)
-{
-    if (!R) return set_error(MOE_ERR_INVALID_ARG, "router is NULL");
-    if (R->hidden < 8 || R->hidden % 8) return set_error(MOE_ERR_INVALID_ARG, "hidden=%d must be a positive multiple of 8", R->hidden);
-    if (R->n_experts < 1 || R->n_experts > 1024) return set_error(MOE_ERR_INVALID_ARG, "n_experts=%d outside [1,1024]", R->n_experts);
-    if (R->score != MOE_SCORE_SIGMOID && R->score != MOE_SCORE_SOFTMAX) return set_error(MOE_ERR_INVALID_ARG, "score=%d unknown", R->score);
-    if (R->n_groups < 1 || R->n_groups > 64 || R->n_experts % R->n_groups)
-        return set_error(MOE_ERR_INVALID_ARG, "n_groups=%d outside [1,64] or not a divisor of n_experts=%d", R->n_groups, R->n_experts);
-    if (R->keep_groups < 1 || R->keep_groups > R->n_groups)
-        return set_error(MOE_ERR_INVALID_ARG, "keep_groups=%d outside [1,n_groups]", R->keep_groups);
-    const int most = R->keep_groups * (R->n_experts / R->n_groups);
-    if (R->top_k < 1 || R->top_k > most || R->top_k > 64)
-        return set_error(MOE_ERR_INVALID_ARG, "top_k=%d outside [1,%d]", R->top_k, most < 64 ? most : 64);
-    if (R->flags & ~MOE_ROUTER_RENORM) return set_error(MOE_ERR_INVALID_ARG, "flags=%#x: unknown bits", R->flags);
-    if (!R->w_router) return set_error(MOE_ERR_INVALID_ARG, "w_router is NULL");
-    if ((uintptr_t)R->w_router % 16 || (uintptr_t)R->bias % 4)
-        return set_error(MOE_ERR_INVALID_ARG, "w_router must be 16-byte and bias 4-byte aligned");
-    return MOE_OK;
-}
 
 // Workspace of a call (p.x_bf16 and p.softmax decide the router)
 size_t scored_ws(ScoredPass &p, char *base)
@@ -100,18 +40,49 @@ size_t scored_ws(ScoredPass &p, char *base)
     return off;
 }
 
-int check_linear(const moe_linear *W)
+// Checks a block, and fills in what p takes from it.
+int check_block(const moe_block *B, int T, BlockPass &p)
 {
-    if (!W) return set_error(MOE_ERR_INVALID_ARG, "linear is NULL");
-    if (W->in_features < 1 || W->in_features > 131071)
-        return set_error(MOE_ERR_INVALID_ARG, "in_features=%d outside [1,131071]", W->in_features);
-    if (W->out_features < 1) return set_error(MOE_ERR_INVALID_ARG, "out_features=%d < 1", W->out_features);
-    if (!W->w || !W->w_scale) return set_error(MOE_ERR_INVALID_ARG, "linear weights are NULL");
-    if ((uintptr_t)W->w % 16 || W->ldw % 16 || W->ldw < W->in_features || W->ldw > ((int64_t)1 << 40))
-        return set_error(MOE_ERR_INVALID_ARG, "w must be 16-byte aligned with ldw=%lld a multiple of 16 of at least in_features",
-                         (long long)W->ldw);
-    if ((uintptr_t)W->w_scale % 4 || (uintptr_t)W->bias % 4)
-        return set_error(MOE_ERR_INVALID_ARG, "w_scale and bias must be 4-byte aligned");
+    if (!B) return set_error(MOE_ERR_INVALID_ARG, "block is NULL");
+    int rc;
+    if ((rc = check_norm(B->norm)) || (rc = check_scored(B->router))) return rc;
+    const moe_layer *L = B->layer;
+    if (!L) return set_error(MOE_ERR_INVALID_ARG, "layer is NULL");
+    if (!act_ok(B->act_n)) return set_error(MOE_ERR_INVALID_ARG, "act_n=%d unknown", B->act_n);
+    if (!B->gate_up != !B->down) return set_error(MOE_ERR_INVALID_ARG, "gate_up and down come together");
+    const int H = B->norm->hidden, E = L->n_experts, k = L->top_k;
+    if (L->hidden != H || B->router->hidden != H) return set_error(MOE_ERR_INVALID_ARG, "norm, router and layer differ in hidden");
+    if (B->router->n_experts != E || B->router->top_k != k) return set_error(MOE_ERR_INVALID_ARG, "router and layer differ in experts or top_k");
+    if (L->inter < 8 || L->inter % 8) return set_error(MOE_ERR_INVALID_ARG, "inter=%d must be a positive multiple of 8", L->inter);
+    if (!L->w_gate || !L->w_up || !L->w_down || !L->codebook) return set_error(MOE_ERR_INVALID_ARG, "layer weights are NULL");
+    if (((uintptr_t)L->w_gate | (uintptr_t)L->w_up | (uintptr_t)L->w_down | (uintptr_t)L->codebook | (uintptr_t)B->norm->weight) % 16)
+        return set_error(MOE_ERR_INVALID_ARG, "the norm's and the layer's weights must be 16-byte aligned");
+    if (L->fmt_gate_up != MOE_FMT_CB2 || L->fmt_down != MOE_FMT_Q2K)
+        return set_error(MOE_ERR_UNSUPPORTED, "formats %d and %d: CB2 gate/up and Q2K down are needed", L->fmt_gate_up, L->fmt_down);
+    if (L->sh_inter || L->flags || L->expert_slot)
+        return set_error(MOE_ERR_UNSUPPORTED, "a layer with a shared expert of its own, flags or an expert map");
+    if (B->gate_up) {
+        if ((rc = check_linear(B->gate_up)) || (rc = check_linear(B->down))) return rc;
+        const int sh = B->down->in_features;
+        if (B->gate_up->in_features != H || B->down->out_features != H || B->gate_up->out_features != 2 * (int64_t)sh)
+            return set_error(MOE_ERR_INVALID_ARG, "shared expert: gate_up %d x %d, down %d x %d do not fit hidden %d", B->gate_up->out_features,
+                             B->gate_up->in_features, B->down->out_features, sh, H);
+        p.sh = sh;
+        p.sh_up = B->gate_up->w; p.ld_up = B->gate_up->ldw; p.up_scale = B->gate_up->w_scale; p.up_bias = B->gate_up->bias;
+        p.sh_down = B->down->w; p.ld_down = B->down->ldw; p.down_scale = B->down->w_scale; p.down_bias = B->down->bias;
+    }
+    if (H > BLOCK_MAX_DIM || L->inter > BLOCK_MAX_DIM || p.sh > BLOCK_MAX_DIM || E > BLOCK_MAX_E || k > BLOCK_MAX_K || T > BLOCK_MAX_T)
+        return set_error(MOE_ERR_UNSUPPORTED, "hidden=%d, inter=%d, shared=%d, n_experts=%d, top_k=%d, T=%d: more than the block takes", H,
+                         L->inter, p.sh, E, k, T);
+    p.T = T; p.H = H; p.I = L->inter; p.E = E; p.k = k;
+    p.n_bf16 = B->act_n == MOE_ACT_BF16; p.norm_w = B->norm->weight; p.eps = B->norm->eps;
+    p.gate = (const uint8_t *)L->w_gate; p.up = (const uint8_t *)L->w_up; p.down = (const uint8_t *)L->w_down;
+    p.codebook = L->codebook;
+    const moe_router *R = B->router;
+    ScoredPass &r = p.route;
+    r.T = T; r.H = H; r.E = E; r.k = k;
+    r.softmax = R->score == MOE_SCORE_SOFTMAX; r.groups = R->n_groups; r.keep = R->keep_groups;
+    r.renorm = (R->flags & MOE_ROUTER_RENORM) != 0; r.scale = R->scale; r.w = R->w_router; r.bias = R->bias;
     return MOE_OK;
 }
 
@@ -190,11 +161,8 @@ int moe_residual_norm(const moe_norm *N, int T, const void *x, int act_x, int64_
                       int act_res, int64_t ldres, void *sum, int64_t ldsum, void *out, int act_out, int64_t ldout,
                       int8_t *q, int64_t ldq, float *q_scale, void *stream, moe_profile *prof)
 {
-    int rc;
-    if (!N) return set_error(MOE_ERR_INVALID_ARG, "norm is NULL");
-    if (N->hidden < 1 || N->hidden > ROWS_MAX) return set_error(MOE_ERR_INVALID_ARG, "hidden=%d outside [1,%d]", N->hidden, ROWS_MAX);
-    if (!(N->eps >= 0.0f)) return set_error(MOE_ERR_INVALID_ARG, "eps=%g is negative or NaN", (double)N->eps);
-    if (!N->weight || (uintptr_t)N->weight % 4) return set_error(MOE_ERR_INVALID_ARG, "weight is NULL or not 4-byte aligned");
+    int rc = check_norm(N);
+    if (rc) return rc;
     if (T < 0) return set_error(MOE_ERR_INVALID_ARG, "T=%d < 0", T);
     if (!act_ok(act_x) || (residual && !act_ok(act_res)) || (out && !act_ok(act_out)))
         return set_error(MOE_ERR_INVALID_ARG, "unknown activation type");
@@ -283,6 +251,50 @@ int moe_linear_i8(const moe_linear *W, int T, const int8_t *x, int64_t ldx, cons
     p.ws = ws;
     Launcher run{prof, (hipStream_t)stream};
     return run("linear_i8", [&] { return launch_linear(p, (hipStream_t)stream); });
+}
+
+size_t moe_block_decode_workspace_bytes(const moe_block *B, int T)
+{
+    BlockPass p{};
+    if (T < 0 || check_block(B, T, p)) return 0;
+    block_layout(p);
+    return block_workspace(p, nullptr);
+}
+
+int moe_block_decode(const moe_block *B, int T, const void *x, int act_x, int64_t ldx, const void *residual, int act_res,
+                     int64_t ldres, void *sum, int64_t ldsum, float *y, int64_t ldy, int32_t *topk_idx, float *topk_w,
+                     int32_t *offsets, int32_t *perm, int32_t *inv, void *ws, size_t ws_bytes, void *stream,
+                     moe_profile *prof)
+{
+    if (T < 0) return set_error(MOE_ERR_INVALID_ARG, "T=%d < 0", T);
+    BlockPass p{};
+    int rc = check_block(B, T, p);
+    if (rc) return rc;
+    if (!act_ok(act_x) || (residual && !act_ok(act_res))) return set_error(MOE_ERR_INVALID_ARG, "unknown activation type");
+    if (prof) prof->n_launches = 0;
+    if (T == 0) return MOE_OK;
+    if (sum && !residual) return set_error(MOE_ERR_INVALID_ARG, "sum without a residual");
+    if ((rc = check_rows("x", x, ldx, T, p.H, act_size(act_x)))) return rc;
+    if (residual && (rc = check_rows("residual", residual, ldres, T, p.H, act_size(act_res)))) return rc;
+    if (sum && (rc = check_rows("sum", sum, ldsum, T, p.H, act_size(act_res)))) return rc;
+    if ((rc = check_rows("y", y, ldy, T, p.H, 4))) return rc;
+    if (!topk_idx || !topk_w || !offsets || !perm || !inv) return set_error(MOE_ERR_INVALID_ARG, "NULL tensor argument");
+    if (!ws) return set_error(MOE_ERR_INVALID_ARG, "workspace is NULL");
+    if (((uintptr_t)x | (uintptr_t)residual | (uintptr_t)sum | (uintptr_t)ws) % 16 || (ldx | (residual ? ldres : 0) | (sum ? ldsum : 0)) % 8)
+        return set_error(MOE_ERR_INVALID_ARG, "x, residual, sum and the workspace must be 16-byte aligned, their strides multiples of 8");
+    block_layout(p);
+    const size_t need = block_workspace(p, (char *)ws);
+    if (ws_bytes < need) return set_error(MOE_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+    p.x = x; p.x_bf16 = act_x == MOE_ACT_BF16; p.ldx = ldx;
+    p.res = residual; p.res_bf16 = act_res == MOE_ACT_BF16; p.ldres = ldres;
+    p.sum = sum; p.ldsum = ldsum;
+    p.y = y; p.ldy = ldy;
+    ScoredPass &r = p.route;
+    r.topk_idx = topk_idx; r.topk_w = topk_w; r.offsets = offsets; r.perm = perm; r.inv = inv;
+    const hipStream_t s = (hipStream_t)stream;
+    Launcher run{prof, s};
+    if ((rc = run("block_norm", [&] { return launch_block_norm(p, s); }))) return rc;
+    return run("block", [&] { return launch_block(p, s); });
 }
 
 }  // extern "C"

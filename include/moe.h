@@ -470,6 +470,44 @@ int moe_linear_i8(const moe_linear *W, int T, const int8_t *x, int64_t ldx, cons
                   moe_profile *prof);
 size_t moe_linear_i8_workspace_bytes(const moe_linear *W, int T);
 
+/* ------------------------------------------------------------ a block for a few tokens
+ * moe_block_decode: one MoE block for up to 16 tokens in two launches (the norm, and
+ * everything else):
+ *     s = x + residual, n = norm(s)  as moe_residual_norm, n rounded to type act_n
+ *     the routing of n               as moe_route_scored, its outputs written
+ *     y = sum_j topk_w[j] * FFN_{topk_idx[j]}(n) + FFN_shared(n)       fp32 [T] rows, ldy apart
+ * where it stands for moe_residual_norm, moe_route_scored, moe_expert_ffn_decode and the
+ * shared expert's int8 linear layers.  Weights are applied exactly and activations with an
+ * error of 2^-24 of the largest value of their 256 neighbours, sums are exact within 256
+ * products and fp32 beyond: y is within a few 2^-22 relative of 64-bit arithmetic on the
+ * same n.  The shared expert's activations are not cut to 8 bits here, so its output
+ * differs from that of moe_linear_i8 on codes by those codes' rounding.  A token's y
+ * depends on the rest of the batch only in the order of fp32 sums.
+ *   B->norm, B->router, B->layer: as in their own calls; the layer without a shared expert of
+ *     its own (sh_inter 0), without flags and expert_slot, CB2 gate/up and Q2K down
+ *     (MOE_ERR_UNSUPPORTED otherwise); its w_router is not read.
+ *   B->gate_up, B->down: NULL both, or the shared expert: gate_up [2 I_s][H] with rows
+ *     [gate | up], down [H][I_s]; biases are added.
+ *   hidden and inter are multiples of 8; hidden, inter and I_s at most 8192, E at most 512, k
+ *     at most 16, T at most 16 (MOE_ERR_UNSUPPORTED otherwise).
+ * x and residual rows, sum and ws 16-byte aligned, strides multiples of 8 elements; sum: NULL
+ * or the residual's type, may be the residual.  Nothing else may overlap.  A workspace of
+ * moe_block_decode_workspace_bytes() for T tokens serves every smaller batch and needs no
+ * clearing, but calls that may overlap in time (two streams, two graphs) need one each: the
+ * call's counters are in it.  (Shared all the same, the calls end and y is wrong or NaN.) */
+typedef struct moe_block {
+    const moe_norm *norm;
+    const moe_router *router;
+    const moe_layer *layer;
+    const moe_linear *gate_up, *down;
+    int32_t act_n;
+} moe_block;
+int moe_block_decode(const moe_block *B, int T, const void *x, int act_x, int64_t ldx, const void *residual, int act_res,
+                     int64_t ldres, void *sum, int64_t ldsum, float *y, int64_t ldy, int32_t *topk_idx, float *topk_w,
+                     int32_t *offsets, int32_t *perm, int32_t *inv, void *ws, size_t ws_bytes, void *stream,
+                     moe_profile *prof);
+size_t moe_block_decode_workspace_bytes(const moe_block *B, int T);
+
 /* ------------------------------------------------------------ pack / unpack
  * q2_pack (host): quantize a row-major fp32 matrix w_host [rows][K] into
  * out_host (q2_packed_bytes(fmt, rows, K) bytes).  fmt: CB2 (needs
