@@ -30,14 +30,15 @@ struct BlockPass {
     uint32_t *ctl;                               // counters, a line each
     int32_t *list;                               // different experts, then a token and a weight for each position
     double *logits;                              // [T][E]
-    float *n;                                    // [T][H]
+    void *s;                                     // [T][H] of the residual's type
     int8_t *planes;                              // [T][quads of H][3072]
     float *scales;                               // [T][4 quads of H]
     float *h, *hs;                               // [T k][Ip], [T][sh]
     // set by block_layout
     int nb, nq, nbi, nqi, nbs, nqs, Ip;          // blocks of 256 and quads of blocks of H, I, sh; row of h
     int F, nf, rows;                             // features of a routed gate/up item, items of an expert, rows of a down item
-    int t_router, t_shared, t_down;              // items
+    int experts;                                 // whose logits a work-group of the first kernel computes
+    int t_shared, t_down;                        // items
     int slots, chunk;                            // tokens, and rows of h, that LDS holds
     int o_planes, o_scales, o_red, lds;          // LDS offsets and bytes
 };

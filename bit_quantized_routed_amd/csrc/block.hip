@@ -3,12 +3,11 @@
 //   s = x + res;  n = rms_norm(s);  scored routing of n;
 //   y = sum_j w_j FFN_{e_j}(n) + FFN_shared(n)
 //
-// The first kernel is the norm.  The second does everything else: its work is cut
-// into items (a router row, 8 features of the shared gate/up, F features of a
-// routed expert's gate/up, some rows of y) that work-groups draw by ticket, in
-// that order, and an item waits only for items of lower tickets: for the
-// selection (made by the work-group that finishes the last router row), for h of
-// all experts.  Tickets are drawn by running work-groups only, so the lowest
+// The first kernel is the norm and the router's logits.  The second does everything
+// else: its work is cut into items (the selection, 8 features of the shared
+// gate/up, F features of a routed expert's gate/up, some rows of y) that
+// work-groups draw by ticket, in that order, and an item waits only for items of
+// lower tickets: for the selection, for h of all experts.  Tickets are drawn by running work-groups only, so the lowest
 // unfinished item is always being worked on and every wait ends, however many
 // work-groups are resident and whatever else runs on the device.  (A bound on
 // the polls ends a wait all the same, should a second call overwrite the
@@ -49,10 +48,29 @@ constexpr int NT = 1024, NW = NT / 64;
 constexpr int QUAD = 3072;                       // bytes of four blocks' digits: [16 steps][4 blocks][3 digits][16]
 constexpr float QMAX = 8323072.0f;               // 127 * 2^16
 constexpr int LINE = 32;                         // uint32s of a counter's line
-enum { C_TICKET = 0, C_ROUTER = LINE, C_LIST = 2 * LINE, C_SHARED = 3 * LINE, C_ROUTED = 4 * LINE, C_WORDS = 5 * LINE };
+enum { C_TICKET = 0, C_LIST = LINE, C_SHARED = 2 * LINE, C_ROUTED = 3 * LINE, C_WORDS = 4 * LINE };
 constexpr int TABLE = 32768;                     // LDS: [256 codewords][16 copies][8 selectors]
 constexpr int O_ZERO = TABLE;                    // zeros for the lanes whose rows of the matrix instruction are empty
-constexpr int O_END = TABLE + QUAD;
+constexpr int O_SMALL = TABLE + QUAD;            // the parts' small arrays
+
+struct Small {
+    union {
+        struct {
+            uint32_t mask[BLOCK_MAX_E];          // tokens of an expert
+            float weight[BLOCK_MAX_T * BLOCK_MAX_K];
+            int32_t sums[2][NW];
+            int16_t chosen[BLOCK_MAX_T * BLOCK_MAX_K], first[BLOCK_MAX_E];
+        } select;
+        struct {
+            int16_t token[4], slot[4], row[4];   // of the tokens in hand: their slots of digits, their rows of h
+        } routed;
+    };
+    // the list: different experts (expert, first position, tokens), and each position's token, weight and expert's number
+    int32_t entry[BLOCK_MAX_T * BLOCK_MAX_K];
+    float weight[BLOCK_MAX_T * BLOCK_MAX_K];
+    int16_t tok[BLOCK_MAX_T * BLOCK_MAX_K], seg[BLOCK_MAX_T * BLOCK_MAX_K];
+};
+constexpr int O_END = O_SMALL + (sizeof(Small) + 15) / 16 * 16;
 
 __device__ __forceinline__ float to_f32(const uint32_t w, int hi) { return __uint_as_float(hi ? w & 0xffff0000u : w << 16); }
 
@@ -60,6 +78,18 @@ template <class T>
 __device__ __forceinline__ T peek(const T *p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 template <class T>
 __device__ __forceinline__ void post(T *p, T v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+// The kernel's parts are functions of their own, so that none's loop invariants and registers weigh on another's (one body
+// took 10 us before its first item, with 1500 instructions on spilled scalars).  Each finds the arguments in the kernel's
+// argument segment and loads what it needs into scalar registers.
+struct Args { uint32_t lo, hi; };
+
+__device__ __forceinline__ const BlockPass &args_of(Args a)
+{
+    const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)a.hi) << 32 |
+                        (uint32_t)__builtin_amdgcn_readfirstlane((int)a.lo);
+    return *(const BlockPass *)(const __attribute__((address_space(4))) BlockPass *)at;
+}
 
 // three signed digits of base 256, least first
 __device__ __forceinline__ void digits(int q, int &d0, int &d1, int &d2)
@@ -84,9 +114,12 @@ __device__ __forceinline__ float block_scale(uint32_t m, float &inv)
     return !finite ? __uint_as_float(0x7fc00000u) : some ? amax / QMAX : 0.0f;
 }
 
-// ---------------------------------------------------------------- norm
-// A work-group a token, 8 elements a thread: the operations of the row kernels'
-// norm, in their order; then the digits of n.  Clears the counters.
+// ---------------------------------------------------------------- norm and logits
+// A work-group a token and a few experts, 8 elements of the token a thread: the
+// operations of the row kernels' norm, in their order, in every work-group of the
+// token; the first of them leaves s and the digits of n.  s goes to the
+// workspace, and where the caller wants it by the second kernel: it may replace
+// the residual, which other work-groups still read here.  Clears the counters.
 __device__ __forceinline__ void load8(const void *p, int bf16, int64_t at, float v[8])
 {
     if (bf16) {
@@ -104,48 +137,61 @@ __device__ __forceinline__ uint32_t bf16_bits(float f) { return __builtin_bit_ca
 
 __global__ __launch_bounds__(NT) void block_norm(BlockPass p)
 {
-    __shared__ double part[NW];
-    const int tid = threadIdx.x, t = blockIdx.x, c = 8 * tid;
-    if (t == 0 && tid < C_WORDS) p.ctl[tid] = 0;
+    __shared__ double part[NW], logit[NW][4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, t = blockIdx.x, c = 8 * tid;
+    const bool lead = blockIdx.y == 0;
+    if (t == 0 && lead && tid < C_WORDS) p.ctl[tid] = 0;
     const bool in = c < p.H;
-    float v[8], g[8];
+    const int at = in ? c : 0;                   // something in bounds
+    const int e0 = blockIdx.y * p.experts, e1 = min(e0 + p.experts, p.E);
+    float v[8], g[8], w[4][8];                   // up to four experts' weights are on their way during the norm
+    auto load_w = [&](int e, float o[8]) {
+        if (e < e1) load8(p.route.w, 0, (int64_t)e * p.H + at, o);
+    };
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = g[j] = 0.0f;
-    if (in) {
-        load8(p.x, p.x_bf16, (int64_t)t * p.ldx + c, v);
-        load8(p.norm_w, 0, c, g);
-        if (p.res) {
-            float r[8];
-            load8(p.res, p.res_bf16, (int64_t)t * p.ldres + c, r);
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[j] = v[j] + r[j];
-                if (p.res_bf16) v[j] = __uint_as_float(bf16_bits(v[j]) << 16);
-            }
-            if (p.sum) {
-                const int64_t at = (int64_t)t * p.ldsum + c;
-                if (p.res_bf16) {
-                    u32x4 u;
+        for (int j = 0; j < 8; ++j) w[i][j] = 0.0f;
+    load8(p.x, p.x_bf16, (int64_t)t * p.ldx + at, v);
+    load8(p.norm_w, 0, at, g);
+    if (p.res) {
+        float r[8];
+        load8(p.res, p.res_bf16, (int64_t)t * p.ldres + at, r);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) u[j] = bf16_bits(v[2 * j]) | bf16_bits(v[2 * j + 1]) << 16;
-                    *(u32x4 *)((uint16_t *)p.sum + at) = u;
-                } else {
-                    *(f32x4 *)((float *)p.sum + at) = f32x4{v[0], v[1], v[2], v[3]};
-                    *(f32x4 *)((float *)p.sum + at + 4) = f32x4{v[4], v[5], v[6], v[7]};
-                }
+        for (int i = 0; i < 4; ++i) load_w(e0 + i, w[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] = v[j] + r[j];
+            if (p.res_bf16) v[j] = __uint_as_float(bf16_bits(v[j]) << 16);
+        }
+        if (p.sum && lead && in) {
+            const int64_t o = (int64_t)t * p.H + c;
+            if (p.res_bf16) {
+                u32x4 u;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) u[j] = bf16_bits(v[2 * j]) | bf16_bits(v[2 * j + 1]) << 16;
+                *(u32x4 *)((uint16_t *)p.s + o) = u;
+            } else {
+                *(f32x4 *)((float *)p.s + o) = f32x4{v[0], v[1], v[2], v[3]};
+                *(f32x4 *)((float *)p.s + o + 4) = f32x4{v[4], v[5], v[6], v[7]};
             }
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_w(e0 + i, w[i]);
     }
     double ss = 0.0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fma((double)v[j], (double)v[j], ss);
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) ss += __shfl_xor(ss, off, 64);
-    if ((tid & 63) == 0) part[tid >> 6] = ss;
+    for (int j = 0; j < 8; ++j) {
+        v[j] = in ? v[j] : 0.0f;
+        ss = fma((double)v[j], (double)v[j], ss);
+    }
+    ss = wave_sum_f64(ss);
+    if (lane == 0) part[wave] = ss;
     __syncthreads();
     ss = part[0];
 #pragma unroll
-    for (int w = 1; w < NW; ++w) ss += part[w];
+    for (int q = 1; q < NW; ++q) ss += part[q];
     const float r = (float)(1.0 / sqrt(ss / (double)p.H + (double)p.eps));
     uint32_t m = 0;
 #pragma unroll
@@ -154,25 +200,46 @@ __global__ __launch_bounds__(NT) void block_norm(BlockPass p)
         if (p.n_bf16) v[j] = __uint_as_float(bf16_bits(v[j]) << 16);
         m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
     }
-    if (in) {
-        float *o = p.n + (int64_t)t * p.H + c;
-        *(f32x4 *)o = f32x4{v[0], v[1], v[2], v[3]};
-        *(f32x4 *)(o + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    if (lead) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));  // the 32 threads of a block
+        if (c < p.nq * 1024) {
+            float inv;
+            const float scale = block_scale(m, inv);
+            if ((tid & 31) == 0) p.scales[t * 4 * p.nq + (tid >> 5)] = scale;
+            int d[8][3];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) digits((int)rintf(v[j] * inv), d[j][2], d[j][1], d[j][0]);
+            // block tid / 32, step tid / 2 % 16, half tid % 2
+            int8_t *o = p.planes + ((int64_t)t * p.nq + (tid >> 7)) * QUAD + ((tid >> 1) & 15) * 192 + ((tid >> 5) & 3) * 48 + (tid & 1) * 8;
+#pragma unroll
+            for (int q = 0; q < 3; ++q)
+                *(uint2 *)(o + 16 * q) = uint2{bytes4(d[0][q], d[1][q], d[2][q], d[3][q]), bytes4(d[4][q], d[5][q], d[6][q], d[7][q])};
+        }
     }
+    // fp64 logits, four experts at a time
+    for (int e = e0; e < e1; e += 4) {
+        if (e > e0) {
+            __syncthreads();                     // the sums are read
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));  // the 32 threads of a block
-    if (c >= p.nq * 1024) return;
-    float inv;
-    const float scale = block_scale(m, inv);
-    if ((tid & 31) == 0) p.scales[t * 4 * p.nq + (tid >> 5)] = scale;
-    int d[8][3];
+            for (int i = 0; i < 4; ++i) load_w(e + i, w[i]);
+        }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) digits((int)rintf(v[j] * inv), d[j][2], d[j][1], d[j][0]);
-    // block tid / 32, step tid / 2 % 16, half tid % 2
-    int8_t *o = p.planes + ((int64_t)t * p.nq + (tid >> 7)) * QUAD + ((tid >> 1) & 15) * 192 + ((tid >> 5) & 3) * 48 + (tid & 1) * 8;
+        for (int i = 0; i < 4; ++i) {
+            if (e + i >= e1) break;
+            double l = 0.0;
 #pragma unroll
-    for (int q = 0; q < 3; ++q)
-        *(uint2 *)(o + 16 * q) = uint2{bytes4(d[0][q], d[1][q], d[2][q], d[3][q]), bytes4(d[4][q], d[5][q], d[6][q], d[7][q])};
+            for (int j = 0; j < 8; ++j) l = fma((double)v[j], in ? (double)w[i][j] : 0.0, l);
+            l = wave_sum_f64(l);
+            if (lane == 0) logit[wave][i] = l;
+        }
+        __syncthreads();
+        if (tid < 4 && e + tid < e1) {
+            double l = logit[0][tid];
+            for (int q = 1; q < NW; ++q) l += logit[q][tid];
+            p.logits[(int64_t)t * p.E + e + tid] = l;
+        }
+    }
 }
 
 // ---------------------------------------------------------------- the rest
@@ -185,6 +252,7 @@ __device__ __forceinline__ i32x4 mfma_i8(const i32x4 &a, const i32x4 &b, const i
 __device__ __forceinline__ float joined(const i32x4 &a) { return fmaf((float)a[0], 65536.0f, (float)(a[1] * 256 + a[2])); }
 
 extern __shared__ __align__(16) int8_t smem[];
+__device__ __forceinline__ Small &small() { return *(Small *)(smem + O_SMALL); }
 
 // Thread 0 waits until *p is at least n; false if that does not come (two seconds or more).
 constexpr int POLLS = 1 << 21;
@@ -198,19 +266,26 @@ __device__ bool wait_for(const uint32_t *p, uint32_t n)
     return false;
 }
 
-// All of a work-group's posts are acknowledged before thread 0 raises the counter.
-__device__ __forceinline__ uint32_t arrive(uint32_t *p)
+// All of a work-group's posts are acknowledged before thread 0 raises the counter (and draws the next ticket with it).
+__device__ __forceinline__ uint32_t draw(uint32_t *ctl)
+{
+    return __hip_atomic_fetch_add(ctl + C_TICKET, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ void arrive(uint32_t *ctl, int counter, uint32_t &next)
 {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    uint32_t before = 0;
-    if (threadIdx.x == 0) before = __hip_atomic_fetch_add(p, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    return before;
+    if (threadIdx.x == 0) {
+        __hip_atomic_fetch_add(ctl + counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        next = draw(ctl);
+    }
 }
 
 // digits and scales of tokens t0 .. t0 + n - 1 (list: of the tokens in it) into LDS slots
-__device__ void stage_tokens(const BlockPass &p, int t0, const int16_t *tokens, int n)
+__device__ __noinline__ void stage_tokens(Args pa, int t0, const int16_t *tokens, int n)
 {
+    const BlockPass &p = args_of(pa);
     const int per = p.nq * (QUAD / 16);
     for (int i = threadIdx.x; i < n * per; i += NT) {
         const int j = i / per, t = tokens ? tokens[j] : t0 + j;
@@ -223,52 +298,25 @@ __device__ void stage_tokens(const BlockPass &p, int t0, const int16_t *tokens, 
     }
 }
 
-// ---- a router row: fp64 logits of one expert
-__device__ void router_item(const BlockPass &p, int e)
-{
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = 8 * tid;
-    double *const part = (double *)(smem + p.o_red);                   // [NW][T]
-    float w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 0.0f;
-    const int at = min(c, p.H - 8);
-    if (c < p.H) load8(p.route.w, 0, (int64_t)e * p.H + c, w);
-    for (int t = 0; t < p.T; ++t) {
-        float v[8];
-        load8(p.n, 0, (int64_t)t * p.H + at, v);
-        double s = 0.0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s = fma(c < p.H ? (double)v[j] : 0.0, (double)w[j], s);
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
-        if (lane == 0) part[wave * BLOCK_MAX_T + t] = s;
-    }
-    __syncthreads();
-    if (tid < p.T) {
-        double s = part[tid];
-        for (int v = 1; v < NW; ++v) s += part[v * BLOCK_MAX_T + tid];
-        post(p.logits + (int64_t)tid * p.E + e, s);
-    }
-}
-
 // ---- the selection: a wave a token, then the grouping and the list of experts
 template <int MAXPL>
-__device__ void select(const BlockPass &p)
+__device__ __noinline__ void select(Args pa)
 {
+    const BlockPass &p = args_of(pa);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int E = p.E, k = p.k, n = p.T * k;
-    __shared__ int16_t chosen[BLOCK_MAX_T * BLOCK_MAX_K];
-    __shared__ float weight[BLOCK_MAX_T * BLOCK_MAX_K];
-    __shared__ uint32_t mask[BLOCK_MAX_E];       // tokens of an expert
-    __shared__ int16_t first[BLOCK_MAX_E];
-    __shared__ int sums[2][NW];
+    auto &mask = small().select.mask;
+    auto &weight = small().select.weight;
+    auto &sums = small().select.sums;
+    auto &chosen = small().select.chosen;
+    auto &first = small().select.first;
     double *const cs = (double *)(smem + p.o_planes);                  // [T][E]
     if (tid < BLOCK_MAX_E) mask[tid] = 0;
     if (wave < p.T) {
         double l[MAXPL], pr[MAXPL], c[MAXPL];
 #pragma unroll
         for (int i = 0; i < MAXPL; ++i)
-            l[i] = lane + 64 * i < E ? peek(p.logits + (int64_t)wave * E + lane + 64 * i) : -INFINITY;
+            l[i] = lane + 64 * i < E ? p.logits[(int64_t)wave * E + lane + 64 * i] : -INFINITY;
         token_scores<MAXPL>(p.route, l, lane, pr, c);
         if (p.route.keep < p.route.groups) {
             const Groups<double> g = rank_groups<MAXPL, double>(p.route, lane, c, cs + wave * E);
@@ -338,8 +386,9 @@ __device__ __forceinline__ i32x4 load_row16(const int8_t *row, int at, int K)
     return v;
 }
 
-__device__ void shared_item(const BlockPass &p, int item, int t0, int nt)
+__device__ __noinline__ void shared_item(Args pa, int item, int t0, int nt)
 {
+    const BlockPass &p = args_of(pa);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
     const int f = 8 * item + (r & 7);
     const int8_t *const row = p.sh_up + (int64_t)((r < 8 ? 0 : p.sh) + min(f, p.sh - 1)) * p.ld_up;
@@ -444,8 +493,10 @@ __device__ __forceinline__ void routed_unit(const BlockPass &p, const Window &gw
 }
 
 template <int N>
-__device__ void routed_units(const BlockPass &p, int e, int f0, int n, const int16_t *slots)
+__device__ __noinline__ void routed_units(Args pa, int e, int f0, int n)
 {
+    const BlockPass &p = args_of(pa);
+    const auto &slots = small().routed.slot;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const int units = p.F / 16 * p.nq;
     const bool in = (r & 3) < 3 && (r >> 2) == g;
@@ -495,33 +546,33 @@ __device__ void routed_units(const BlockPass &p, int e, int f0, int n, const int
             a += x[0];
             u += x[16];
         }
-        // row of h: the position, which slots[] is followed by
-        if (f0 + f < p.I) post(p.h + (int64_t)slots[BLOCK_MAX_T + j] * p.Ip + f0 + f, a / (1.0f + expf(-a)) * u);
+        if (f0 + f < p.I) post(p.h + (int64_t)small().routed.row[j] * p.Ip + f0 + f, a / (1.0f + expf(-a)) * u);
     }
 }
 
-__device__ void routed_item(const BlockPass &p, int item, bool &resident)
+__device__ __noinline__ void routed_item(Args pa, int item)
 {
-    __shared__ int16_t tokens[2 * BLOCK_MAX_T], slots[2 * BLOCK_MAX_T];
+    const BlockPass &p = args_of(pa);
+    auto &now = small().routed;
     const int d = item / p.nf, f0 = item % p.nf * p.F;
-    const int entry = peek(p.list + d), e = entry & 1023, first = entry >> 10 & 1023, n = entry >> 20;
+    const int entry = small().entry[d], e = entry & 1023, first = entry >> 10 & 1023, n = entry >> 20;
     for (int j0 = 0; j0 < n; j0 += 4) {
         const int m = min(4, n - j0);
         __syncthreads();
         if (threadIdx.x < m) {
-            tokens[threadIdx.x] = (int16_t)peek(p.list + 256 + first + j0 + threadIdx.x);
-            slots[threadIdx.x] = p.T <= p.slots ? tokens[threadIdx.x] : (int16_t)threadIdx.x;
-            slots[BLOCK_MAX_T + threadIdx.x] = (int16_t)(first + j0 + threadIdx.x);
+            const int i = threadIdx.x, t = small().tok[first + j0 + i];
+            now.token[i] = (int16_t)t;
+            now.slot[i] = (int16_t)(p.T <= p.slots ? t : i);
+            now.row[i] = (int16_t)(first + j0 + i);
         }
         __syncthreads();
         if (p.T > p.slots) {
-            stage_tokens(p, 0, tokens, m);
-            resident = false;
+            stage_tokens(pa, 0, now.token, m);
             __syncthreads();
         }
-        if (m == 1) routed_units<1>(p, e, f0, m, slots);
-        else if (m == 2) routed_units<2>(p, e, f0, m, slots);
-        else routed_units<4>(p, e, f0, m, slots);
+        if (m == 1) routed_units<1>(pa, e, f0, m);
+        else if (m == 2) routed_units<2>(pa, e, f0, m);
+        else routed_units<4>(pa, e, f0, m);
     }
 }
 
@@ -529,7 +580,7 @@ __device__ void routed_item(const BlockPass &p, int item, bool &resident)
 // Digits of rows of h into LDS: row i (of `count`) is at src + i * ld, n elements; natural order, or for Q2_K dword j of a step =
 // weights j, j + 4, j + 8, j + 12, with the sums of its 16 sub-blocks in four digits.
 template <bool Q2K>
-__device__ void stage_h(const BlockPass &p, const float *src, int64_t ld, int count, int n, int nq)
+__device__ __forceinline__ void stage_h(const BlockPass &p, const float *src, int64_t ld, int count, int n, int nq)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, grp = lane >> 2, j = lane & 3;
     const int nb = 4 * nq;
@@ -589,6 +640,7 @@ __device__ __forceinline__ void down_unit(const uint32_t c[21], const int8_t *co
     for (int n = 0; n < N; ++n) acc[n] = i32x4{0, 0, 0, 0};
 #pragma unroll
     for (int s = 0; s < 16; ++s) {
+        __builtin_amdgcn_sched_barrier(0);       // few of the steps' LDS reads in registers at once
         const uint32_t sc = (c[1 + s / 4] >> (8 * (s & 3))) & 15u, q = c[5 + s];
         const uint32_t pool = sc * 0x020100u | sc * 3u << 24;
         i32x4 w;
@@ -607,8 +659,7 @@ __device__ __forceinline__ void down_unit(const uint32_t c[21], const int8_t *co
 // N rows of h from i0 on (LDS rows) with 16 rows of one expert's down matrix and a quad of its blocks, times the rows' weights,
 // onto this wave's sums
 template <int N>
-__device__ void down_rows(const BlockPass &p, const uint32_t c[21], int count, int i0, int n, int quad, const int32_t *tok,
-                          const float *weight, float *ya)
+__device__ __forceinline__ void down_rows(const BlockPass &p, const uint32_t c[21], int count, int c0, int i0, int n, int quad, float *ya)
 {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, nb = 4 * p.nqi, b = 4 * quad + g;
     const int8_t *const planes = smem + p.o_planes, *const sums = planes + count * p.nqi * QUAD;
@@ -635,185 +686,210 @@ __device__ void down_rows(const BlockPass &p, const uint32_t c[21], int count, i
         }
         v += __shfl_xor(v, 16, 64);
         v += __shfl_xor(v, 32, 64);
-        if (g == 0 && j < n) ya[tok[i0 + j] * 32 + r] += weight[i0 + j] * v;
+        if (g == 0 && j < n) ya[small().tok[c0 + i0 + j] * 32 + r] += small().weight[c0 + i0 + j] * v;
     }
 }
 
-__device__ bool down_item(const BlockPass &p, int item, int n_list)
+struct DownBlock { uint32_t c[21]; };
+
+// The down phase of a work-group, item after item; false if a wait was given up.  An item is p.rows rows of y.  Its weights
+// do not hang on h: a wave's first blocks are on their way before the waits.
+__device__ __forceinline__ bool down_items(const BlockPass &p, int item, int base, int n_list, uint32_t &next, uint32_t &word)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
-    __shared__ int32_t tok[BLOCK_MAX_T * BLOCK_MAX_K], entry[BLOCK_MAX_T * BLOCK_MAX_K];
-    __shared__ float weight[BLOCK_MAX_T * BLOCK_MAX_K];
-    __shared__ int ok;
-    const int r0 = item * p.rows, tiles = (p.rows + 15) / 16, n = p.T * p.k;
+    const int tiles = (p.rows + 15) / 16, n = p.T * p.k, units = p.nqi * tiles;
     float *const ya_all = (float *)(smem + p.o_red), *const ya = ya_all + wave * p.T * 32;     // [NW][T][32]
-    __syncthreads();
-    for (int i = lane; i < p.T * 32; i += 64) ya[i] = 0.0f;
-    if (tid < n_list) entry[tid] = peek(p.list + tid);
-    if (tid < n) {
-        tok[tid] = peek(p.list + 256 + tid);
-        weight[tid] = peek((const float *)p.list + 512 + tid);
-    }
-    if (p.sh) {
-        if (tid == 0) ok = wait_for(p.ctl + C_SHARED, (uint32_t)p.t_shared);
-        __syncthreads();
-        if (!ok) return false;
-        const int rows_max = min(p.chunk, p.T), parts = (p.nbs + 1) / 2;
-        for (int t0 = 0; t0 < p.T; t0 += rows_max) {
-            const int nt = min(rows_max, p.T - t0);
-            __syncthreads();
-            stage_h<false>(p, p.hs + (int64_t)t0 * p.sh, p.sh, nt, p.sh, p.nqs);
-            __syncthreads();
-            const float *const sc = (const float *)(smem + p.o_planes + nt * p.nqs * QUAD);
-            for (int u = wave; u < tiles * parts; u += NW) {
-                const int tile = u % tiles, part = u / tiles;
-                const int row = min(r0 + tile * 16 + r, p.H - 1);
-                const int8_t *const wr = p.sh_down + (int64_t)row * p.ld_down;
-                const float ws = p.down_scale[row];
-                i32x4 w[2][4];
+    bool first = true;                           // the waits are still to come
+    while (item < p.t_down) {
+        const int r0 = item * p.rows;
+        auto load_down = [&](int v, int lo) {    // unit v: expert lo + v / units, quad of blocks, tile
+            const int u = v % units, e = small().entry[lo + v / units] & 1023;
+            const int row = min(r0 + u % tiles * 16 + r, p.H - 1), b = min(4 * (u / tiles) + g, p.nbi - 1);
+            const uint32_t *const at = (const uint32_t *)(p.down + (((int64_t)e * p.H + row) * p.nbi + b) * 84);
+            DownBlock x;
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
+            for (int i = 0; i < 5; ++i) {
+                const u32x4u q = *(const u32x4u *)(at + 4 * i);
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) w[q][s] = load_row16(wr, 512 * part + 256 * q + 64 * s + 16 * g, p.sh);
-                for (int tg = 0; tg < nt; tg += 4) {
-                    const int slot = tg + (r >> 2), digit = r & 3, tt = tg + g;
-                    float v = 0.0f;
+                for (int j = 0; j < 4; ++j) x.c[4 * i + j] = q[j];
+            }
+            x.c[20] = at[20];
+            return x;
+        };
+        for (int i = lane; i < p.T * 32; i += 64) ya[i] = 0.0f;
+        if (p.sh) {
+            i32x4 w[4];
+            float ws = 0.0f;
+            auto load_shared = [&](int u) {      // unit u: tile, block
+                const int row = min(r0 + u % tiles * 16 + r, p.H - 1);
+                ws = p.down_scale[row];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int b = 2 * part + q;
-                        const bool in = digit < 3 && slot < nt && b < 4 * p.nqs;
+                for (int s = 0; s < 4; ++s) w[s] = load_row16(p.sh_down + (int64_t)row * p.ld_down, 256 * (u / tiles) + 64 * s + 16 * g, p.sh);
+            };
+            if (wave < tiles * p.nbs) load_shared(wave);
+            if (first) {
+                if (tid == 0) word = wait_for(p.ctl + C_SHARED, (uint32_t)p.t_shared);
+                __syncthreads();
+                if (!word) return false;
+            }
+            const int rows_max = min(p.chunk, p.T);
+            for (int t0 = 0; t0 < p.T; t0 += rows_max) {
+                const int nt = min(rows_max, p.T - t0);
+                __syncthreads();
+                stage_h<false>(p, p.hs + (int64_t)t0 * p.sh, p.sh, nt, p.sh, p.nqs);
+                __syncthreads();
+                const float *const sc = (const float *)(smem + p.o_planes + nt * p.nqs * QUAD);
+                for (int u = wave; u < tiles * p.nbs; u += NW) {
+                    if (u != wave || t0) load_shared(u);
+                    const int tile = u % tiles, b = u / tiles;
+                    for (int tg = 0; tg < nt; tg += 4) {
+                        const int slot = tg + (r >> 2), digit = r & 3, tt = tg + g;
+                        const bool in = digit < 3 && slot < nt;
                         const int8_t *const a =
                             digit_base(p, in, slot, p.nqs * QUAD, (b >> 2) * QUAD + g * 192 + ((b & 3) * 3 + digit) * 16);
                         i32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-                        for (int s = 0; s < 4; ++s) acc = mfma_i8(*(const i32x4 *)(a + s * 768), w[q][s], acc);
-                        if (tt < nt && b < 4 * p.nqs) v = fmaf(joined(acc), sc[tt * 4 * p.nqs + b], v);
+                        for (int s = 0; s < 4; ++s) acc = mfma_i8(*(const i32x4 *)(a + s * 768), w[s], acc);
+                        if (tt < nt) ya[(t0 + tt) * 32 + tile * 16 + r] += joined(acc) * (sc[tt * 4 * p.nqs + b] * ws);
                     }
-                    if (tt < nt) ya[(t0 + tt) * 32 + tile * 16 + r] += v * ws;
                 }
             }
         }
-    }
-    if (tid == 0) ok = wait_for(p.ctl + C_ROUTED, (uint32_t)(n_list * p.nf));
-    __syncthreads();
-    if (!ok) return false;
-    for (int c0 = 0; c0 < n; c0 += p.chunk) {
-        const int count = min(p.chunk, n - c0);
-        __syncthreads();
-        stage_h<true>(p, p.h + (int64_t)c0 * p.Ip, p.Ip, count, p.I, p.nqi);
-        __syncthreads();
-        // units (expert, quad of blocks, tile) dealt to the waves in turn
-        int unit = 0;
-        for (int d = 0; d < n_list; ++d) {
-            const int e = entry[d] & 1023, first = entry[d] >> 10 & 1023;
-            const int lo = max(first, c0), hi = min(first + (entry[d] >> 20), c0 + count);
-            if (lo >= hi) continue;
-            const int units = p.nqi * tiles;
-            for (int u = (wave - unit % NW + NW) % NW; u < units; u += NW) {
-                const int tile = u % tiles, quad = u / tiles;
-                const int row = min(r0 + tile * 16 + r, p.H - 1), b = min(4 * quad + g, p.nbi - 1);
-                const uint32_t *const at = (const uint32_t *)(p.down + (((int64_t)e * p.H + row) * p.nbi + b) * 84);
-                uint32_t c[21];
-#pragma unroll
-                for (int i = 0; i < 5; ++i) {
-                    const u32x4u v = *(const u32x4u *)(at + 4 * i);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) c[4 * i + q] = v[q];
-                }
-                c[20] = at[20];
-                for (int j = lo; j < hi; j += 4) {
-                    const int m = min(4, hi - j);
-                    const int32_t *const tk = tok + c0;
-                    const float *const wt = weight + c0;
-                    if (m == 1) down_rows<1>(p, c, count, j - c0, m, quad, tk, wt, ya + tile * 16);
-                    else if (m == 2) down_rows<2>(p, c, count, j - c0, m, quad, tk, wt, ya + tile * 16);
-                    else down_rows<4>(p, c, count, j - c0, m, quad, tk, wt, ya + tile * 16);
-                }
+        for (int c0 = 0; c0 < n; c0 += p.chunk) {
+            const int count = min(p.chunk, n - c0);
+            const int lo = small().seg[c0], total = (small().seg[c0 + count - 1] + 1 - lo) * units;
+            DownBlock x;
+            if (wave < total) x = load_down(wave, lo);
+            if (first) {
+                if (tid == 0) word = wait_for(p.ctl + C_ROUTED, (uint32_t)(n_list * p.nf));
+                __syncthreads();
+                if (!word) return false;
+                first = false;
             }
-            unit += units;
+            __syncthreads();
+            stage_h<true>(p, p.h + (int64_t)c0 * p.Ip, p.Ip, count, p.I, p.nqi);
+            __syncthreads();
+            for (int v = wave; v < total; v += NW) {
+                const DownBlock now = x;
+                if (v + NW < total) x = load_down(v + NW, lo);
+                const int u = v % units, tile = u % tiles, quad = u / tiles, entry = small().entry[lo + v / units];
+                const int begin = max(entry >> 10 & 1023, c0), end = min((entry >> 10 & 1023) + (entry >> 20), c0 + count);
+                for (int j = begin; j < end; j += 2) down_rows<2>(p, now.c, count, c0, j - c0, min(2, end - j), quad, ya + tile * 16);
+            }
         }
-    }
-    __syncthreads();
-    for (int i = tid; i < p.T * p.rows; i += NT) {
-        const int t = i / p.rows, row = i % p.rows;
-        if (r0 + row >= p.H) continue;
-        float v = ya_all[t * 32 + row];
-        for (int w = 1; w < NW; ++w) v += ya_all[(w * p.T + t) * 32 + row];
-        if (p.sh && p.down_bias) v += p.down_bias[r0 + row];
-        p.y[(int64_t)t * p.ldy + r0 + row] = v;
+        __syncthreads();
+        if (tid == 0) next = draw(p.ctl);
+        for (int i = tid; i < p.T * p.rows; i += NT) {
+            const int t = i / p.rows, row = i % p.rows;
+            if (r0 + row >= p.H) continue;
+            float v = ya_all[t * 32 + row];
+            for (int w = 1; w < NW; ++w) v += ya_all[(w * p.T + t) * 32 + row];
+            if (p.sh && p.down_bias) v += p.down_bias[r0 + row];
+            p.y[(int64_t)t * p.ldy + r0 + row] = v;
+            if (p.sum) {
+                const int64_t from = (int64_t)t * p.H + r0 + row, to = (int64_t)t * p.ldsum + r0 + row;
+                if (p.res_bf16) ((uint16_t *)p.sum)[to] = ((const uint16_t *)p.s)[from];
+                else ((float *)p.sum)[to] = ((const float *)p.s)[from];
+            }
+        }
+        __syncthreads();
+        item = (int)next - base;
+        __syncthreads();                         // and the sums are read
     }
     return true;
 }
 
-template <int MAXPL>
-__global__ __launch_bounds__(NT) void block_kernel(BlockPass p)
+// selectors of the codewords, 16 copies (a lane reads copy lane % 16: no two of 16 lanes share a bank), and the zeros
+__device__ __noinline__ void tables(Args pa)
 {
-    __shared__ uint32_t next, word;
-    const int tid = threadIdx.x;
-    // selectors of the codewords, 16 copies (a lane reads copy lane % 16: no two of 16 lanes share a bank)
-    for (int i = tid; i < 4096; i += NT) {
+    const BlockPass &p = args_of(pa);
+    for (int i = threadIdx.x; i < 4096; i += NT) {
         const uint2 c = *(const uint2 *)(p.codebook + 8 * (i >> 4));
         // (C + 3) / 2 of bytes -3, -1, 1, 3, added without a carry into the next byte
         auto code = [](uint32_t v) { return (((v & 0x7f7f7f7fu) + 0x03030303u) ^ (v & 0x80808080u)) >> 1 & 0x03030303u; };
         *(uint2 *)(smem + 8 * i) = uint2{code(c.x), code(c.y)};
     }
-    for (int i = tid; i < QUAD / 4; i += NT) ((uint32_t *)(smem + O_ZERO))[i] = 0;
-    uint32_t ticket = 0;
-    if (tid == 0) next = __hip_atomic_fetch_add(p.ctl + C_TICKET, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    bool resident = false, ok = true;
-    int n_list = -1;
+    for (int i = threadIdx.x; i < QUAD / 4; i += NT) ((uint32_t *)(smem + O_ZERO))[i] = 0;
+}
+
+__device__ __noinline__ void give_up(Args pa)
+{
+    const BlockPass &p = args_of(pa);
+    for (int i = threadIdx.x; i < p.T * p.H; i += NT) p.y[(int64_t)(i / p.H) * p.ldy + i % p.H] = __uint_as_float(0x7fc00000u);
+}
+
+// the list into LDS
+__device__ __noinline__ void load_list(Args pa, int n_list)
+{
+    const BlockPass &p = args_of(pa);
+    const int tid = threadIdx.x;
+    Small &l = small();
+    if (tid < n_list) {
+        const int entry = peek(p.list + tid);
+        l.entry[tid] = entry;
+        for (int i = 0; i < entry >> 20; ++i) l.seg[(entry >> 10 & 1023) + i] = (int16_t)tid;
+    }
+    if (tid < p.T * p.k) {
+        l.tok[tid] = (int16_t)peek(p.list + 256 + tid);
+        l.weight[tid] = peek((const float *)p.list + 512 + tid);
+    }
+    __syncthreads();
+}
+
+__global__ __launch_bounds__(NT) void block_kernel(BlockPass p)
+{
+    __shared__ uint32_t next, word;
+    const int tid = threadIdx.x;
+    const uint64_t at = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+    const Args pa{(uint32_t)at, (uint32_t)(at >> 32)};
+    uint32_t *const ctl = p.ctl;
+    if (tid == 0) next = draw(ctl);
+    tables(pa);
+    bool resident = false;                       // all tokens' digits are in LDS
+    int n_list = -1, base = 0, item;
     for (;;) {
         __syncthreads();
-        ticket = next;
+        item = (int)next;
         __syncthreads();
-        uint32_t after = 0;
-        if (tid == 0) after = __hip_atomic_fetch_add(p.ctl + C_TICKET, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        int item = (int)ticket;
-        if (item < p.t_router) {
-            router_item(p, item);
-            if (tid == 0) word = 0;
-            const uint32_t before = arrive(p.ctl + C_ROUTER);
-            if (tid == 0) word = before + 1 == (uint32_t)p.t_router;
-            __syncthreads();
-            if (word) {
-                select<MAXPL>(p);
-                resident = false;
-            }
-        } else if ((item -= p.t_router) < p.t_shared) {
+        if (item == 0) {
+            if (p.E <= 256) select<4>(pa);
+            else select<8>(pa);
+            if (tid == 0) next = draw(ctl);
+            continue;
+        }
+        item -= 1;
+        if (item < p.t_shared) {
             for (int t0 = 0; t0 < p.T; t0 += p.slots) {
+                const int nt = min(p.slots, p.T - t0);
                 if (!resident) {
                     __syncthreads();
-                    stage_tokens(p, t0, nullptr, min(p.slots, p.T - t0));
+                    stage_tokens(pa, t0, nullptr, nt);
                     resident = p.T <= p.slots;
                     __syncthreads();
                 }
-                shared_item(p, item, t0, min(p.slots, p.T - t0));
+                shared_item(pa, item, t0, nt);
             }
-            arrive(p.ctl + C_SHARED);
-        } else {
-            item -= p.t_shared;
-            if (n_list < 0) {
-                if (tid == 0) word = wait_for(p.ctl + C_LIST, 1) ? peek(p.ctl + C_LIST) : 0;
-                __syncthreads();
-                n_list = (int)word;
-                ok = n_list > 0;
-            }
-            if (ok && item < n_list * p.nf) {
-                if (!resident && p.T <= p.slots) {
-                    stage_tokens(p, 0, nullptr, p.T);
-                    resident = true;
-                }
-                routed_item(p, item, resident);
-                arrive(p.ctl + C_ROUTED);
-            } else if (ok && (item -= n_list * p.nf) < p.t_down) ok = down_item(p, item, n_list);
-            else if (ok) return;
-            if (!ok) {
-                for (int i = tid; i < p.T * p.H; i += NT) p.y[(int64_t)(i / p.H) * p.ldy + i % p.H] = __uint_as_float(0x7fc00000u);
-                return;
-            }
+            arrive(ctl, C_SHARED, next);
+            continue;
         }
-        if (tid == 0) next = after;
+        if (n_list < 0) {
+            if (!resident && p.T <= p.slots) {
+                stage_tokens(pa, 0, nullptr, p.T);
+                resident = true;
+            }
+            if (tid == 0) word = wait_for(ctl + C_LIST, 1) ? peek(ctl + C_LIST) : 0;
+            __syncthreads();
+            n_list = (int)word;
+            if (n_list == 0) break;
+            load_list(pa, n_list);
+            base = 1 + p.t_shared + n_list * p.nf;
+        }
+        item -= p.t_shared;
+        if (item >= n_list * p.nf) break;
+        routed_item(pa, item);
+        arrive(ctl, C_ROUTED, next);
     }
+    if (n_list == 0 || !down_items(p, item - n_list * p.nf, base, n_list, next, word)) give_up(pa);
 }
 
 }  // namespace
@@ -829,16 +905,16 @@ void block_layout(BlockPass &p)
     p.nf = up(p.I, p.F);
     const int cus = cu_count();
     p.rows = std::min(32, std::max(16, up(p.H, cus)));
-    p.t_router = p.E;
+    p.experts = std::max(1, up(p.E * p.T, 256));
     p.t_shared = up(p.sh, 8);
     p.t_down = up(p.H, p.rows);
     p.slots = std::min(p.T, 4);
     // LDS: table, zeros, planes (or rows of h), scales, sums
     const int units = p.F / 16 * p.nq;
-    const int red = std::max({units * (p.slots <= 2 ? p.slots : 4) * 128, NW * 64 * 4, NW * BLOCK_MAX_T * 8, NW * p.T * 128});
+    const int red = std::max({units * (p.slots <= 2 ? p.slots : 4) * 128, NW * 64 * 4, NW * p.T * 128});
     const int scales = p.slots * 4 * p.nq * 4;
     const int row_i = p.nqi * (QUAD + 4 * 64 + 16), row_s = p.nqs * (QUAD + 16), row = std::max(row_i, row_s);
-    constexpr int LDS = 160 * 1024 - 8192;       // the static shared memory is apart
+    constexpr int LDS = 160 * 1024 - 256;        // the static shared memory is apart
     const int want = std::max({p.slots * p.nq * QUAD + scales, std::min(16, p.T * p.k) * row, p.T * p.E * 8});
     const int room = LDS - O_END - red;
     const int area = std::min(want, room) / 16 * 16;
@@ -860,7 +936,7 @@ size_t block_workspace(BlockPass &p, char *base)
     p.ctl = (uint32_t *)take(C_WORDS * 4);
     p.list = (int32_t *)take(768 * 4);
     p.logits = (double *)take((size_t)p.T * p.E * 8);
-    p.n = (float *)take((size_t)p.T * p.H * 4);
+    p.s = take((size_t)p.T * p.H * 4);
     p.planes = (int8_t *)take((size_t)p.T * p.nq * QUAD);
     p.scales = (float *)take((size_t)p.T * 4 * p.nq * 4);
     p.h = (float *)take((size_t)p.T * p.k * p.Ip * 4);
@@ -870,23 +946,17 @@ size_t block_workspace(BlockPass &p, char *base)
 
 hipError_t launch_block_norm(const BlockPass &p, hipStream_t s)
 {
-    block_norm<<<p.T, NT, 0, s>>>(p);
+    block_norm<<<dim3((unsigned)p.T, (unsigned)((p.E + p.experts - 1) / p.experts)), NT, 0, s>>>(p);
     return hipGetLastError();
 }
 
 hipError_t launch_block(const BlockPass &p, hipStream_t s)
 {
     const unsigned grid = (unsigned)cu_count();  // one work-group's LDS fills a CU
-#define MOE_BLOCK(pl)                                                                             \
-    do {                                                                                          \
-        static DevSlots slots{};                                                                  \
-        const hipError_t e = lds_limit((const void *)block_kernel<pl>, slots, p.lds);             \
-        if (e != hipSuccess) return e;                                                            \
-        block_kernel<pl><<<grid, NT, p.lds, s>>>(p);                                              \
-    } while (0)
-    if (p.E <= 256) MOE_BLOCK(4);
-    else MOE_BLOCK(8);
-#undef MOE_BLOCK
+    static DevSlots slots{};
+    const hipError_t e = lds_limit((const void *)block_kernel, slots, p.lds);
+    if (e != hipSuccess) return e;
+    block_kernel<<<grid, NT, p.lds, s>>>(p);
     return hipGetLastError();
 }
 
