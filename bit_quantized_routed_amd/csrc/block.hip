@@ -44,7 +44,8 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(4)));
 
-constexpr int NT = 1024, NW = NT / 64;
+constexpr int NORM_NT = 1024, NORM_NW = NORM_NT / 64;
+constexpr int NT = 512, NW = NT / 64;
 constexpr int QUAD = 3072;                       // bytes of four blocks' digits: [16 steps][4 blocks][3 digits][16]
 constexpr float QMAX = 8323072.0f;               // 127 * 2^16
 constexpr int LINE = 32;                         // uint32s of a counter's line
@@ -135,9 +136,9 @@ __device__ __forceinline__ void load8(const void *p, int bf16, int64_t at, float
 
 __device__ __forceinline__ uint32_t bf16_bits(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 
-__global__ __launch_bounds__(NT) void block_norm(BlockPass p)
+__global__ __launch_bounds__(NORM_NT) void block_norm(BlockPass p)
 {
-    __shared__ double part[NW], logit[NW][4];
+    __shared__ double part[NORM_NW], logit[NORM_NW][4];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, t = blockIdx.x, c = 8 * tid;
     const bool lead = blockIdx.y == 0;
     if (t == 0 && lead && tid < C_WORDS) p.ctl[tid] = 0;
@@ -191,7 +192,7 @@ __global__ __launch_bounds__(NT) void block_norm(BlockPass p)
     __syncthreads();
     ss = part[0];
 #pragma unroll
-    for (int q = 1; q < NW; ++q) ss += part[q];
+    for (int q = 1; q < NORM_NW; ++q) ss += part[q];
     const float r = (float)(1.0 / sqrt(ss / (double)p.H + (double)p.eps));
     uint32_t m = 0;
 #pragma unroll
@@ -236,7 +237,7 @@ __global__ __launch_bounds__(NT) void block_norm(BlockPass p)
         __syncthreads();
         if (tid < 4 && e + tid < e1) {
             double l = logit[0][tid];
-            for (int q = 1; q < NW; ++q) l += logit[q][tid];
+            for (int q = 1; q < NORM_NW; ++q) l += logit[q][tid];
             p.logits[(int64_t)t * p.E + e + tid] = l;
         }
     }
@@ -312,14 +313,14 @@ __device__ __noinline__ void select(Args pa)
     auto &first = small().select.first;
     double *const cs = (double *)(smem + p.o_planes);                  // [T][E]
     if (tid < BLOCK_MAX_E) mask[tid] = 0;
-    if (wave < p.T) {
+    for (int t = wave; t < p.T; t += NW) {
         double l[MAXPL], pr[MAXPL], c[MAXPL];
 #pragma unroll
         for (int i = 0; i < MAXPL; ++i)
-            l[i] = lane + 64 * i < E ? p.logits[(int64_t)wave * E + lane + 64 * i] : -INFINITY;
+            l[i] = lane + 64 * i < E ? p.logits[(int64_t)t * E + lane + 64 * i] : -INFINITY;
         token_scores<MAXPL>(p.route, l, lane, pr, c);
         if (p.route.keep < p.route.groups) {
-            const Groups<double> g = rank_groups<MAXPL, double>(p.route, lane, c, cs + wave * E);
+            const Groups<double> g = rank_groups<MAXPL, double>(p.route, lane, c, cs + t * E);
             const float inv = 1.0f / (float)(E / p.route.groups);
 #pragma unroll
             for (int i = 0; i < MAXPL; ++i)
@@ -329,10 +330,10 @@ __device__ __noinline__ void select(Args pa)
         double my_c, my_p;
         uint32_t taken;
         select64<MAXPL>(p.route, lane, c, pr, my_e, my_c, my_p, taken);
-        const float w = write_token(p.route, wave, lane, my_e, lane < k && my_c != -INFINITY ? my_p : 0.0);
+        const float w = write_token(p.route, t, lane, my_e, lane < k && my_c != -INFINITY ? my_p : 0.0);
         if (lane < k) {
-            chosen[wave * k + lane] = (int16_t)my_e;
-            weight[wave * k + lane] = w;
+            chosen[t * k + lane] = (int16_t)my_e;
+            weight[t * k + lane] = w;
         }
     }
     __syncthreads();
@@ -774,7 +775,11 @@ __device__ __forceinline__ bool down_items(const BlockPass &p, int item, int bas
                 if (v + NW < total) x = load_down(v + NW, lo);
                 const int u = v % units, tile = u % tiles, quad = u / tiles, entry = small().entry[lo + v / units];
                 const int begin = max(entry >> 10 & 1023, c0), end = min((entry >> 10 & 1023) + (entry >> 20), c0 + count);
-                for (int j = begin; j < end; j += 2) down_rows<2>(p, now.c, count, c0, j - c0, min(2, end - j), quad, ya + tile * 16);
+                for (int j = begin; j < end; j += 4) {
+                    const int m = min(4, end - j);
+                    if (m == 1) down_rows<1>(p, now.c, count, c0, j - c0, m, quad, ya + tile * 16);
+                    else down_rows<4>(p, now.c, count, c0, j - c0, m, quad, ya + tile * 16);
+                }
             }
         }
         __syncthreads();
@@ -946,7 +951,7 @@ size_t block_workspace(BlockPass &p, char *base)
 
 hipError_t launch_block_norm(const BlockPass &p, hipStream_t s)
 {
-    block_norm<<<dim3((unsigned)p.T, (unsigned)((p.E + p.experts - 1) / p.experts)), NT, 0, s>>>(p);
+    block_norm<<<dim3((unsigned)p.T, (unsigned)((p.E + p.experts - 1) / p.experts)), NORM_NT, 0, s>>>(p);
     return hipGetLastError();
 }
 
