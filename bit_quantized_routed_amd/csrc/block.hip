@@ -106,6 +106,29 @@ __device__ __forceinline__ uint32_t bytes4(int a, int b, int c, int d)
     return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
 }
 
+// sum over the lanes r, r + 16, r + 32, r + 48
+__device__ __forceinline__ float sum_rows(float v)
+{
+    uint32_t u = __float_as_uint(v);
+    auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    u = __float_as_uint(__uint_as_float(a[0]) + __uint_as_float(a[1]));
+    a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+// largest of the wave's non-negative integers: four steps within rows of 16 lanes, then across them
+__device__ __forceinline__ uint32_t max_bits(uint32_t v)
+{
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false));      // quad_perm [1,0,3,2]
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false));      // quad_perm [2,3,0,1]
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false));     // row_half_mirror
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false));     // row_mirror
+    auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max(a[0], a[1]);
+    a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return max(a[0], a[1]);
+}
+
 // scale and its reciprocal for a block whose largest magnitude has the bits m (an infinity or a NaN wins, and makes the scale NaN)
 __device__ __forceinline__ float block_scale(uint32_t m, float &inv)
 {
@@ -531,10 +554,8 @@ __device__ __noinline__ void routed_units(Args pa, int e, int f0, int n)
         for (int j = 0; j < N; ++j) {
             const float s = b < p.nb && j < n ? sc[slots[min(j, n - 1)] * 4 * p.nq + b] : 0.0f;
             float x = b < p.nb ? joined(ag[j]) * (dg * s) : 0.0f, y = b < p.nb ? joined(au[j]) * (du * s) : 0.0f;
-            x += __shfl_xor(x, 16, 64);
-            y += __shfl_xor(y, 16, 64);
-            x += __shfl_xor(x, 32, 64);
-            y += __shfl_xor(y, 32, 64);
+            x = sum_rows(x);
+            y = sum_rows(y);
             if (g < 2) red[(u * N + j) * 32 + lane] = g ? y : x;
         }
     }
@@ -587,7 +608,7 @@ __device__ __forceinline__ void stage_h(const BlockPass &p, const float *src, in
     const int nb = 4 * nq;
     int8_t *const planes = smem + p.o_planes, *const sums = planes + count * nq * QUAD;
     float *const sc = (float *)(sums + (Q2K ? count * nb * 64 : 0));
-    constexpr int B = 4;
+    constexpr int B = 8;
     for (int i0 = wave; i0 < count * nb; i0 += B * NW) {
         float v[B][4];
 #pragma unroll
@@ -596,7 +617,7 @@ __device__ __forceinline__ void stage_h(const BlockPass &p, const float *src, in
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int at = f + (Q2K ? 4 * c : c);
-                v[q][c] = i < count * nb && at < n ? peek(src + row * ld + at) : 0.0f;
+                v[q][c] = i < count * nb && at < n ? (Q2K ? src[row * ld + at] : peek(src + row * ld + at)) : 0.0f;
             }
         }
 #pragma unroll
@@ -607,8 +628,7 @@ __device__ __forceinline__ void stage_h(const BlockPass &p, const float *src, in
             uint32_t m = 0;
 #pragma unroll
             for (int c = 0; c < 4; ++c) m = max(m, __float_as_uint(v[q][c]) & 0x7fffffffu);
-#pragma unroll
-            for (int off = 32; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
+            m = max_bits(m);
             float inv;
             const float scale = block_scale(m, inv);
             int x[4], d[4][3];
@@ -622,8 +642,8 @@ __device__ __forceinline__ void stage_h(const BlockPass &p, const float *src, in
             for (int c = 0; c < 3; ++c) *(uint32_t *)(o + 16 * c) = bytes4(d[0][c], d[1][c], d[2][c], d[3][c]);
             if (Q2K) {
                 int s = x[0] + x[1] + x[2] + x[3];
-                s += __shfl_xor(s, 1, 64);
-                s += __shfl_xor(s, 2, 64);
+                s += __builtin_amdgcn_mov_dpp(s, 0xB1, 0xF, 0xF, false);
+                s += __builtin_amdgcn_mov_dpp(s, 0x4E, 0xF, 0xF, false);
                 int d0, d1, d2, d3 = (int)(int8_t)s;
                 digits((s - d3) >> 8, d2, d1, d0);
                 sums[(row * nb + b) * 64 + 16 * j + grp] = (int8_t)(j == 0 ? d0 : j == 1 ? d1 : j == 2 ? d2 : d3);
@@ -641,7 +661,6 @@ __device__ __forceinline__ void down_unit(const uint32_t c[21], const int8_t *co
     for (int n = 0; n < N; ++n) acc[n] = i32x4{0, 0, 0, 0};
 #pragma unroll
     for (int s = 0; s < 16; ++s) {
-        __builtin_amdgcn_sched_barrier(0);       // few of the steps' LDS reads in registers at once
         const uint32_t sc = (c[1 + s / 4] >> (8 * (s & 3))) & 15u, q = c[5 + s];
         const uint32_t pool = sc * 0x020100u | sc * 3u << 24;
         i32x4 w;
@@ -685,8 +704,7 @@ __device__ __forceinline__ void down_rows(const BlockPass &p, const uint32_t c[2
             const float off = fmaf((float)(mins[j][0] * 256 + mins[j][1]), 65536.0f, (float)(mins[j][2] * 256 + mins[j][3]));
             v = joined(acc[j]) * (d * s) - off * (dmin * s);
         }
-        v += __shfl_xor(v, 16, 64);
-        v += __shfl_xor(v, 32, 64);
+        v = sum_rows(v);
         if (g == 0 && j < n) ya[small().tok[c0 + i0 + j] * 32 + r] += small().weight[c0 + i0 + j] * v;
     }
 }
