@@ -33,14 +33,15 @@ struct BlockPass {
     void *s;                                     // [T][H] of the residual's type
     int8_t *planes;                              // [T][quads of H][3072]
     float *scales;                               // [T][4 quads of H]
-    float *h, *hs;                               // [T k][Ip], [T][sh]
+    int8_t *h;                                   // [T k][records] of 64 features in digits
+    float *hs;                                   // [T][sh]
     // set by block_layout
-    int nb, nq, nbi, nqi, nbs, nqs, Ip;          // blocks of 256 and quads of blocks of H, I, sh; row of h
+    int nb, nq, nbi, nqi, nbs, nqs, records;     // blocks of 256 and quads of blocks of H, I, sh; records of a row of h
     int F, nf, rows;                             // features of a routed gate/up item, items of an expert, rows of a down item
     int experts;                                 // whose logits a work-group of the first kernel computes
     int t_shared, t_down;                        // items
     int slots, chunk;                            // tokens, and rows of h, that LDS holds
-    int o_planes, o_scales, o_red, lds;          // LDS offsets and bytes
+    int o_planes, o_scales, o_red, o_recs, lds;          // LDS offsets and bytes
 };
 
 void block_layout(BlockPass &p);                 // the sizes that follow from the first line

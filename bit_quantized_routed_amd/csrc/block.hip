@@ -48,6 +48,10 @@ constexpr int NORM_NT = 1024, NORM_NW = NORM_NT / 64;
 constexpr int NT = 512, NW = NT / 64;
 constexpr int QUAD = 3072;                       // bytes of four blocks' digits: [16 steps][4 blocks][3 digits][16]
 constexpr float QMAX = 8323072.0f;               // 127 * 2^16
+// 64 features of a row of h: [4 steps][3 digits][16] in the order of Q2_K's codes (dword i of a step = features i, i + 4, i + 8,
+// i + 12), the sums of the four steps (fp32) and the scale.  A record has lines of its own in the workspace; in LDS four
+// records are a block's, a little apart from the next block's for the banks' sake.
+constexpr int REC = 224, REC_SUMS = 192, REC_SCALE = 208, REC_LINES = 256, REC_BLOCK = 4 * REC + 48;
 constexpr int LINE = 32;                         // uint32s of a counter's line
 enum { C_TICKET = 0, C_LIST = LINE, C_SHARED = 2 * LINE, C_ROUTED = 3 * LINE, C_WORDS = 4 * LINE };
 constexpr int TABLE = 32768;                     // LDS: [256 codewords][16 copies][8 selectors]
@@ -560,15 +564,37 @@ __device__ __noinline__ void routed_units(Args pa, int e, int f0, int n)
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n * p.F; i += NT) {
-        const int j = i / p.F, f = i % p.F;
+    // a wave finishes 64 features of a token: SwiGLU, digits, sums
+    const int groups = p.F / 64;
+    for (int i = wave; i < n * groups; i += NW) {
+        const int j = i / groups, f = i % groups * 64 + lane;
         float a = 0.0f, u = 0.0f;
         for (int q = 0; q < p.nq; ++q) {
             const float *const x = red + ((f / 16 * p.nq + q) * N + j) * 32 + f % 16;
             a += x[0];
             u += x[16];
         }
-        if (f0 + f < p.I) post(p.h + (int64_t)small().routed.row[j] * p.Ip + f0 + f, a / (1.0f + expf(-a)) * u);
+        const float h = f0 + f < p.I ? a / (1.0f + expf(-a)) * u : 0.0f;
+        float inv;
+        const float scale = block_scale(max_bits(__float_as_uint(h) & 0x7fffffffu), inv);
+        int x = (int)rintf(h * inv), d0, d1, d2;
+        digits(x, d2, d1, d0);
+        // bytes to their places by way of LDS
+        int8_t *const rec = smem + p.o_recs + wave * REC;
+        int8_t *const o = rec + (lane >> 4) * 48 + 4 * (lane & 3) + (lane >> 2 & 3);
+        o[0] = (int8_t)d0;
+        o[16] = (int8_t)d1;
+        o[32] = (int8_t)d2;
+        x += __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, false);       // the 16 lanes of a step
+        x += __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, false);
+        x += __builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, false);
+        x += __builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, false);
+        if ((lane & 15) == 0) ((float *)(rec + REC_SUMS))[lane >> 4] = (float)x * scale;
+        if (lane == 0) *(float *)(rec + REC_SCALE) = scale;
+        wave_sync();
+        if (lane < REC / 4)
+            post((uint32_t *)(p.h + ((int64_t)small().routed.row[j] * p.records + (f0 + f) / 64) * REC_LINES) + lane, ((const uint32_t *)rec)[lane]);
+        wave_sync();
     }
 }
 
@@ -599,113 +625,95 @@ __device__ __noinline__ void routed_item(Args pa, int item)
 }
 
 // ---- some rows of y: the shared expert's down rows and every chosen expert's
-// Digits of rows of h into LDS: row i (of `count`) is at src + i * ld, n elements; natural order, or for Q2_K dword j of a step =
-// weights j, j + 4, j + 8, j + 12, with the sums of its 16 sub-blocks in four digits.
-template <bool Q2K>
-__device__ __forceinline__ void stage_h(const BlockPass &p, const float *src, int64_t ld, int count, int n, int nq)
+// Digits of rows of the shared expert's h into LDS.
+__device__ __forceinline__ void stage_shared(const BlockPass &p, int t0, int count)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, grp = lane >> 2, j = lane & 3;
-    const int nb = 4 * nq;
-    int8_t *const planes = smem + p.o_planes, *const sums = planes + count * nq * QUAD;
-    float *const sc = (float *)(sums + (Q2K ? count * nb * 64 : 0));
-    constexpr int B = 8;
-    for (int i0 = wave; i0 < count * nb; i0 += B * NW) {
-        float v[B][4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int nb = 4 * p.nqs;
+    int8_t *const planes = smem + p.o_planes;
+    float *const sc = (float *)(planes + count * p.nqs * QUAD);
+    for (int i = wave; i < count * nb; i += NW) {
+        const int row = i / nb, b = i - row * nb, at = 256 * b + 4 * lane;
+        float v[4];
 #pragma unroll
-        for (int q = 0; q < B; ++q) {
-            const int i = i0 + q * NW, row = i / nb, f = 256 * (i - row * nb) + 16 * grp + (Q2K ? j : 4 * j);
+        for (int c = 0; c < 4; ++c) v[c] = at + c < p.sh ? peek(p.hs + (int64_t)(t0 + row) * p.sh + at + c) : 0.0f;
+        uint32_t m = 0;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int at = f + (Q2K ? 4 * c : c);
-                v[q][c] = i < count * nb && at < n ? (Q2K ? src[row * ld + at] : peek(src + row * ld + at)) : 0.0f;
-            }
-        }
+        for (int c = 0; c < 4; ++c) m = max(m, __float_as_uint(v[c]) & 0x7fffffffu);
+        float inv;
+        const float scale = block_scale(max_bits(m), inv);
+        int d[4][3];
 #pragma unroll
-        for (int q = 0; q < B; ++q) {
-            const int i = i0 + q * NW;
-            if (i >= count * nb) break;
-            const int row = i / nb, b = i - row * nb;
-            uint32_t m = 0;
+        for (int c = 0; c < 4; ++c) digits((int)rintf(v[c] * inv), d[c][2], d[c][1], d[c][0]);
+        int8_t *const o = planes + (row * p.nqs + (b >> 2)) * QUAD + (lane >> 2) * 192 + (b & 3) * 48 + 4 * (lane & 3);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) m = max(m, __float_as_uint(v[q][c]) & 0x7fffffffu);
-            m = max_bits(m);
-            float inv;
-            const float scale = block_scale(m, inv);
-            int x[4], d[4][3];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                x[c] = (int)rintf(v[q][c] * inv);
-                digits(x[c], d[c][2], d[c][1], d[c][0]);
-            }
-            int8_t *const o = planes + (row * nq + (b >> 2)) * QUAD + grp * 192 + (b & 3) * 48 + 4 * j;
-#pragma unroll
-            for (int c = 0; c < 3; ++c) *(uint32_t *)(o + 16 * c) = bytes4(d[0][c], d[1][c], d[2][c], d[3][c]);
-            if (Q2K) {
-                int s = x[0] + x[1] + x[2] + x[3];
-                s += __builtin_amdgcn_mov_dpp(s, 0xB1, 0xF, 0xF, false);
-                s += __builtin_amdgcn_mov_dpp(s, 0x4E, 0xF, 0xF, false);
-                int d0, d1, d2, d3 = (int)(int8_t)s;
-                digits((s - d3) >> 8, d2, d1, d0);
-                sums[(row * nb + b) * 64 + 16 * j + grp] = (int8_t)(j == 0 ? d0 : j == 1 ? d1 : j == 2 ? d2 : d3);
-            }
-            if (lane == 0) sc[row * nb + b] = scale;
-        }
+        for (int c = 0; c < 3; ++c) *(uint32_t *)(o + 16 * c) = bytes4(d[0][c], d[1][c], d[2][c], d[3][c]);
+        if (lane == 0) sc[i] = scale;
     }
 }
 
-template <int N>
-__device__ __forceinline__ void down_unit(const uint32_t c[21], const int8_t *const a[N], const int8_t *const m[N], i32x4 acc[N],
-                                          i32x4 min_acc[N])
+// Records of `count` rows of h from c0 on into LDS; what no item has written (past inter) is zero.
+__device__ __forceinline__ void stage_h(const BlockPass &p, int c0, int count)
 {
-#pragma unroll
-    for (int n = 0; n < N; ++n) acc[n] = i32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int s = 0; s < 16; ++s) {
-        const uint32_t sc = (c[1 + s / 4] >> (8 * (s & 3))) & 15u, q = c[5 + s];
-        const uint32_t pool = sc * 0x020100u | sc * 3u << 24;
-        i32x4 w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = (int)__builtin_amdgcn_perm(pool, pool, q >> (2 * i) & 0x03030303u);
-#pragma unroll
-        for (int n = 0; n < N; ++n) acc[n] = mfma_i8(*(const i32x4 *)(a[n] + s * 192), w, acc[n]);
+    constexpr int PIECES = REC / 16;
+    const int per_row = p.nqi * 16;              // records of a row in LDS
+    int8_t *const planes = smem + p.o_planes;
+    // a record is shared out over 16 threads, the last two idle
+    for (int i = threadIdx.x; i < count * per_row * 16; i += NT) {
+        const int rec = i >> 4, piece = i & 15, row = rec / per_row, at = rec - row * per_row;
+        if (piece >= PIECES) continue;
+        u32x4 v = {0, 0, 0, 0};
+        if (at < p.records) v = *(const u32x4 *)(p.h + ((int64_t)(c0 + row) * p.records + at) * REC_LINES + 16 * piece);
+        *(u32x4 *)(planes + (row * p.nqi * 4 + (at >> 2)) * REC_BLOCK + (at & 3) * REC + 16 * piece) = v;
     }
-    i32x4 w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = (int)(c[1 + i] >> 4 & 0x0f0f0f0fu);
-#pragma unroll
-    for (int n = 0; n < N; ++n) min_acc[n] = mfma_i8(*(const i32x4 *)m[n], w, i32x4{0, 0, 0, 0});
 }
 
 // N rows of h from i0 on (LDS rows) with 16 rows of one expert's down matrix and a quad of its blocks, times the rows' weights,
 // onto this wave's sums
 template <int N>
-__device__ __forceinline__ void down_rows(const BlockPass &p, const uint32_t c[21], int count, int c0, int i0, int n, int quad, float *ya)
+__device__ __forceinline__ void down_rows(const BlockPass &p, const uint32_t c[21], int c0, int i0, int n, int quad, float *ya)
 {
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, nb = 4 * p.nqi, b = 4 * quad + g;
-    const int8_t *const planes = smem + p.o_planes, *const sums = planes + count * p.nqi * QUAD;
-    const float *const sc = (const float *)(sums + count * nb * 64);
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, b = 4 * quad + g;
+    const int8_t *const planes = smem + p.o_planes;
     const int beta = r >> 2, digit = r & 3;
-    const int8_t *a[N], *m[N];
+    const int8_t *a[N], *rec[N];
+    float v[N], off[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        const int row = i0 + min(j, n - 1);
-        const bool in = beta == g && j < n;
-        a[j] = in && digit < 3 ? planes + (row * p.nqi + quad) * QUAD + (beta * 3 + digit) * 16 : smem + O_ZERO;
-        m[j] = in ? sums + (row * nb + b) * 64 + 16 * digit : smem + O_ZERO;
+        const int row = (i0 + min(j, n - 1)) * p.nqi * 4;
+        a[j] = beta == g && digit < 3 ? planes + (row + 4 * quad + beta) * REC_BLOCK + digit * 16 : smem + O_ZERO;
+        rec[j] = planes + (row + b) * REC_BLOCK;
+        v[j] = off[j] = 0.0f;
     }
-    i32x4 acc[N], mins[N];
-    down_unit<N>(c, a, m, acc, mins);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {                // 64 features with a scale of their own
+        i32x4 acc[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] = i32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t sc = (c[1 + q] >> (8 * i)) & 15u, code = c[5 + 4 * q + i];
+            const uint32_t pool = sc * 0x020100u | sc * 3u << 24;
+            i32x4 w;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = (int)__builtin_amdgcn_perm(pool, pool, code >> (2 * k) & 0x03030303u);
+#pragma unroll
+            for (int j = 0; j < N; ++j) acc[j] = mfma_i8(*(const i32x4 *)(a[j] + q * REC + i * 48), w, acc[j]);
+        }
+        const uint32_t m = c[1 + q] >> 4 & 0x0f0f0f0fu;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const f32x4 s = *(const f32x4 *)(rec[j] + q * REC + REC_SUMS);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) off[j] = fmaf((float)(m >> (8 * i) & 255u), s[i], off[j]);
+            v[j] = fmaf(joined(acc[j]), *(const float *)(rec[j] + q * REC + REC_SCALE), v[j]);
+        }
+    }
     const float d = f16_bits_to_f32(c[0] & 0xffffu), dmin = f16_bits_to_f32(c[0] >> 16);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        float v = 0.0f;
-        if (b < p.nbi && j < n) {
-            const float s = sc[(i0 + j) * nb + b];
-            const float off = fmaf((float)(mins[j][0] * 256 + mins[j][1]), 65536.0f, (float)(mins[j][2] * 256 + mins[j][3]));
-            v = joined(acc[j]) * (d * s) - off * (dmin * s);
-        }
-        v = sum_rows(v);
-        if (g == 0 && j < n) ya[small().tok[c0 + i0 + j] * 32 + r] += small().weight[c0 + i0 + j] * v;
+        const float x = sum_rows(b < p.nbi && j < n ? v[j] * d - off[j] * dmin : 0.0f);
+        if (g == 0 && j < n) ya[small().tok[c0 + i0 + j] * 32 + r] += small().weight[c0 + i0 + j] * x;
     }
 }
 
@@ -755,7 +763,7 @@ __device__ __forceinline__ bool down_items(const BlockPass &p, int item, int bas
             for (int t0 = 0; t0 < p.T; t0 += rows_max) {
                 const int nt = min(rows_max, p.T - t0);
                 __syncthreads();
-                stage_h<false>(p, p.hs + (int64_t)t0 * p.sh, p.sh, nt, p.sh, p.nqs);
+                stage_shared(p, t0, nt);
                 __syncthreads();
                 const float *const sc = (const float *)(smem + p.o_planes + nt * p.nqs * QUAD);
                 for (int u = wave; u < tiles * p.nbs; u += NW) {
@@ -777,8 +785,9 @@ __device__ __forceinline__ bool down_items(const BlockPass &p, int item, int bas
         for (int c0 = 0; c0 < n; c0 += p.chunk) {
             const int count = min(p.chunk, n - c0);
             const int lo = small().seg[c0], total = (small().seg[c0 + count - 1] + 1 - lo) * units;
-            DownBlock x;
+            DownBlock x, x1;
             if (wave < total) x = load_down(wave, lo);
+            if (wave + NW < total) x1 = load_down(wave + NW, lo);
             if (first) {
                 if (tid == 0) word = wait_for(p.ctl + C_ROUTED, (uint32_t)(n_list * p.nf));
                 __syncthreads();
@@ -786,18 +795,21 @@ __device__ __forceinline__ bool down_items(const BlockPass &p, int item, int bas
                 first = false;
             }
             __syncthreads();
-            stage_h<true>(p, p.h + (int64_t)c0 * p.Ip, p.Ip, count, p.I, p.nqi);
+            stage_h(p, c0, count);
             __syncthreads();
-            for (int v = wave; v < total; v += NW) {
-                const DownBlock now = x;
-                if (v + NW < total) x = load_down(v + NW, lo);
+            auto unit = [&](int v, const DownBlock &now) {
                 const int u = v % units, tile = u % tiles, quad = u / tiles, entry = small().entry[lo + v / units];
                 const int begin = max(entry >> 10 & 1023, c0), end = min((entry >> 10 & 1023) + (entry >> 20), c0 + count);
-                for (int j = begin; j < end; j += 4) {
-                    const int m = min(4, end - j);
-                    if (m == 1) down_rows<1>(p, now.c, count, c0, j - c0, m, quad, ya + tile * 16);
-                    else down_rows<4>(p, now.c, count, c0, j - c0, m, quad, ya + tile * 16);
+                for (int j = begin; j < end; j += 2) {
+                    if (end - j == 1) down_rows<1>(p, now.c, c0, j - c0, 1, quad, ya + tile * 16);
+                    else down_rows<2>(p, now.c, c0, j - c0, 2, quad, ya + tile * 16);
                 }
+            };
+            for (int v = wave; v < total; v += 2 * NW) {
+                unit(v, x);
+                if (v + 2 * NW < total) x = load_down(v + 2 * NW, lo);
+                if (v + NW < total) unit(v + NW, x1);
+                if (v + 3 * NW < total) x1 = load_down(v + 3 * NW, lo);
             }
         }
         __syncthreads();
@@ -923,9 +935,9 @@ void block_layout(BlockPass &p)
     p.nb = up(p.H, 256); p.nq = up(p.nb, 4);
     p.nbi = up(p.I, 256); p.nqi = up(p.nbi, 4);
     p.nbs = up(p.sh, 256); p.nqs = up(p.nbs, 4);
-    p.Ip = up(p.I, 32) * 32;
     p.F = p.nq >= 4 ? 64 : 128;
     p.nf = up(p.I, p.F);
+    p.records = p.nf * p.F / 64;
     const int cus = cu_count();
     p.rows = std::min(32, std::max(16, up(p.H, cus)));
     p.experts = std::max(1, up(p.E * p.T, 256));
@@ -934,9 +946,10 @@ void block_layout(BlockPass &p)
     p.slots = std::min(p.T, 4);
     // LDS: table, zeros, planes (or rows of h), scales, sums
     const int units = p.F / 16 * p.nq;
-    const int red = std::max({units * (p.slots <= 2 ? p.slots : 4) * 128, NW * 64 * 4, NW * p.T * 128});
+    const int sums = std::max({units * (p.slots <= 2 ? p.slots : 4) * 128, NW * 64 * 4, NW * p.T * 128});
+    const int red = sums + NW * REC;             // and the waves' records
     const int scales = p.slots * 4 * p.nq * 4;
-    const int row_i = p.nqi * (QUAD + 4 * 64 + 16), row_s = p.nqs * (QUAD + 16), row = std::max(row_i, row_s);
+    const int row_i = p.nqi * 4 * REC_BLOCK, row_s = p.nqs * (QUAD + 16), row = std::max(row_i, row_s);
     constexpr int LDS = 160 * 1024 - 256;        // the static shared memory is apart
     const int want = std::max({p.slots * p.nq * QUAD + scales, std::min(16, p.T * p.k) * row, p.T * p.E * 8});
     const int room = LDS - O_END - red;
@@ -945,6 +958,7 @@ void block_layout(BlockPass &p)
     p.o_planes = O_END;
     p.o_scales = O_END + p.slots * p.nq * QUAD;
     p.o_red = O_END + area;
+    p.o_recs = p.o_red + sums;
     p.lds = O_END + area + red;
 }
 
@@ -962,7 +976,7 @@ size_t block_workspace(BlockPass &p, char *base)
     p.s = take((size_t)p.T * p.H * 4);
     p.planes = (int8_t *)take((size_t)p.T * p.nq * QUAD);
     p.scales = (float *)take((size_t)p.T * 4 * p.nq * 4);
-    p.h = (float *)take((size_t)p.T * p.k * p.Ip * 4);
+    p.h = (int8_t *)take((size_t)p.T * p.k * p.records * REC_LINES);
     p.hs = (float *)take((size_t)p.T * p.sh * 4);
     return off;
 }
