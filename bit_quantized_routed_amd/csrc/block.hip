@@ -42,6 +42,7 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(4)));
 
 constexpr int NORM_NT = 1024, NORM_NW = NORM_NT / 64;
@@ -690,13 +691,16 @@ __device__ __forceinline__ void down_rows(const BlockPass &p, const uint32_t c[2
         i32x4 acc[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) acc[j] = i32x4{0, 0, 0, 0};
+        const uint32_t sc = c[1 + q] & 0x0f0f0f0fu;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t sc = (c[1 + q] >> (8 * i)) & 15u, code = c[5 + 4 * q + i];
-            const uint32_t pool = sc * 0x020100u | sc * 3u << 24;
+            uint32_t code = c[5 + 4 * q + i];
+            asm volatile("" : "+v"(code));       // expanded here, not once for all rows: the registers are not there
+            // four codes of 2 bits in the bytes, times the scale in both halves: at most 45, no carry between bytes
+            const u16x2 s = __builtin_bit_cast(u16x2, __builtin_amdgcn_perm(sc, sc, 0x0c000c00u | 0x00010001u * i));
             i32x4 w;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = (int)__builtin_amdgcn_perm(pool, pool, code >> (2 * k) & 0x03030303u);
+            for (int k = 0; k < 4; ++k) w[k] = __builtin_bit_cast(int, (u16x2)(__builtin_bit_cast(u16x2, code >> (2 * k) & 0x03030303u) * s));
 #pragma unroll
             for (int j = 0; j < N; ++j) acc[j] = mfma_i8(*(const i32x4 *)(a[j] + q * REC + i * 48), w, acc[j]);
         }
