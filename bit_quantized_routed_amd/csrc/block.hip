@@ -55,7 +55,7 @@ constexpr float QMAX = 8323072.0f;               // 127 * 2^16
 constexpr int REC = 224, REC_SUMS = 192, REC_SCALE = 208, REC_LINES = 256, REC_BLOCK = 4 * REC + 48;
 constexpr int LINE = 32;                         // uint32s of a counter's line
 enum { C_TICKET = 0, C_LIST = LINE, C_SHARED = 2 * LINE, C_ROUTED = 3 * LINE, C_WORDS = 4 * LINE };
-constexpr int TABLE = 32768;                     // LDS: [256 codewords][16 copies][8 selectors]
+constexpr int TABLE = 32768;                     // LDS: [256 codewords][16 copies]
 constexpr int O_ZERO = TABLE;                    // zeros for the lanes whose rows of the matrix instruction are empty
 constexpr int O_SMALL = TABLE + QUAD;            // the parts' small arrays
 
@@ -68,7 +68,7 @@ struct Small {
             int16_t chosen[BLOCK_MAX_T * BLOCK_MAX_K], first[BLOCK_MAX_E];
         } select;
         struct {
-            int16_t token[4], slot[4], row[4];   // of the tokens in hand: their slots of digits, their rows of h
+            int16_t token[2], slot[2], row[2];   // of the tokens in hand: their slots of digits, their rows of h
         } routed;
     };
     // the list: different experts (expert, first position, tokens), and each position's token, weight and expert's number
@@ -475,56 +475,43 @@ struct Cb2 {
         scales = __builtin_amdgcn_perm(v.w[1], v.w[0], sel);
         d = f16_bits_to_f32((odd ? v.w[0] >> 16 : v.w[0]) & 0xffffu);
     }
-    // the bytes -3 s, -s, s, 3 s of sub-block j: 0x80 - b, its top bit flipped, is -b without a borrow into the next byte
-    __device__ __forceinline__ uint32_t pool(int j) const
-    {
-        const uint32_t s = (scales >> (4 * j)) & 15u;
-        return ((0x8080u - s * 0x0103u) ^ 0x8080u) | s * 0x0301u << 16;
-    }
+    __device__ __forceinline__ int scale(int j) const { return (int)(scales >> (4 * j) & 15u); }
 };
 
+// The codewords go to the matrix instructions as they are, the sums of a sub-block are multiplied by its s_j: three products
+// a token instead of eight permuted dwords of scaled weights.
 template <int N>
-__device__ __forceinline__ void routed_unit(const BlockPass &p, const Window &gw, const Window &uw, bool godd, bool uodd,
-                                            const int8_t *const a[N], i32x4 ag[N], i32x4 au[N], float &dg, float &du)
+__device__ __forceinline__ void routed_unit(const Cb2 &gb, const Cb2 &ub, const int8_t *const a[N], i32x4 ag[N], i32x4 au[N])
 {
-    const Cb2 gb(gw, godd), ub(uw, uodd);
     const uint32_t copy = (threadIdx.x & 15) * 8;
-    auto code = [&](uint32_t idx, int b) {
-        const uint32_t at = ((b == 0 ? idx << 7 : idx >> (8 * b - 7)) & 0x7f80u) | copy;
-        return *(const uint2 *)(smem + at);
+    auto codes = [&](uint32_t idx, int q) {      // codewords 2 q and 2 q + 1 of a sub-block
+        const uint32_t at0 = ((q == 0 ? idx << 7 : idx >> 9) & 0x7f80u) | copy, at1 = (idx >> (16 * q + 1) & 0x7f80u) | copy;
+        const uint2 x = *(const uint2 *)(smem + at0), y = *(const uint2 *)(smem + at1);
+        return i32x4{(int)x.x, (int)x.y, (int)y.x, (int)y.y};
     };
 #pragma unroll
     for (int n = 0; n < N; ++n) ag[n] = au[n] = i32x4{0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const uint32_t gp = gb.pool(j), upool = ub.pool(j);
+        if (N > 1) __builtin_amdgcn_sched_barrier(0);                  // few sub-blocks' LDS reads in registers at once
+        const i32x4 g0 = codes(gb.idx[j], 0), g1 = codes(gb.idx[j], 1), u0 = codes(ub.idx[j], 0), u1 = codes(ub.idx[j], 1);
+        const int gs = gb.scale(j), us = ub.scale(j);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            i32x4 w[2];
+        for (int n = 0; n < N; ++n) {
+            const i32x4 x0 = *(const i32x4 *)(a[n] + 2 * j * 192), x1 = *(const i32x4 *)(a[n] + (2 * j + 1) * 192);
+            const i32x4 g = mfma_i8(x1, g1, mfma_i8(x0, g0, i32x4{0, 0, 0, 0})), u = mfma_i8(x1, u1, mfma_i8(x0, u0, i32x4{0, 0, 0, 0}));
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint2 x = code(gb.idx[j], 2 * q + i), y = code(ub.idx[j], 2 * q + i);
-                w[0][2 * i] = (int)__builtin_amdgcn_perm(gp, gp, x.x);
-                w[0][2 * i + 1] = (int)__builtin_amdgcn_perm(gp, gp, x.y);
-                w[1][2 * i] = (int)__builtin_amdgcn_perm(upool, upool, y.x);
-                w[1][2 * i + 1] = (int)__builtin_amdgcn_perm(upool, upool, y.y);
-            }
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                const i32x4 x = *(const i32x4 *)(a[n] + (2 * j + q) * 192);
-                ag[n] = mfma_i8(x, w[0], ag[n]);
-                au[n] = mfma_i8(x, w[1], au[n]);
+            for (int i = 0; i < 3; ++i) {
+                ag[n][i] += __mul24(g[i], gs);
+                au[n][i] += __mul24(u[i], us);
             }
         }
     }
-    dg = gb.d;
-    du = ub.d;
 }
 
 template <int N>
-__device__ __noinline__ void routed_units(Args pa, int e, int f0, int n)
+__device__ __forceinline__ void routed_units(const BlockPass &p, int e, int f0, int n)
 {
-    const BlockPass &p = args_of(pa);
     const auto &slots = small().routed.slot;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const int units = p.F / 16 * p.nq;
@@ -535,35 +522,36 @@ __device__ __noinline__ void routed_units(Args pa, int e, int f0, int n)
         const int row = min(f0 + u / p.nq * 16 + r, p.I - 1), b = min(4 * (u % p.nq) + g, p.nb - 1);
         return w + (((int64_t)e * p.I + row) * p.nb + b) * 38;
     };
-    Window gw, uw;
-    if (wave < units) {
-        gw = load_window(block_at(p.gate, wave));
-        uw = load_window(block_at(p.up, wave));
-    }
-    for (int u = wave; u < units; u += NW) {
-        const Window g0 = gw, u0 = uw;
-        const bool godd = (uintptr_t)block_at(p.gate, u) & 2, uodd = (uintptr_t)block_at(p.up, u) & 2;
-        if (u + NW < units) {
-            gw = load_window(block_at(p.gate, u + NW));
-            uw = load_window(block_at(p.up, u + NW));
+    struct Pair { Window g, u; };
+    auto load = [&](int u, Pair &w) {
+        if (u < units) {
+            w.g = load_window(block_at(p.gate, u));
+            w.u = load_window(block_at(p.up, u));
         }
+    };
+    // the next unit's blocks are requested before this one's arithmetic
+    auto unit = [&](int u, Pair &w) {
+        const Cb2 gb(w.g, (uintptr_t)block_at(p.gate, u) & 2), ub(w.u, (uintptr_t)block_at(p.up, u) & 2);
+        load(u + NW, w);
         const int q = u % p.nq, b = 4 * q + g;
         const int8_t *a[N];
         i32x4 ag[N], au[N];
 #pragma unroll
         for (int j = 0; j < N; ++j)
             a[j] = digit_base(p, in && j < n, slots[min(j, n - 1)], p.nq * QUAD, q * QUAD + ((r >> 2) * 3 + (r & 3)) * 16);
-        float dg, du;
-        routed_unit<N>(p, g0, u0, godd, uodd, a, ag, au, dg, du);
+        routed_unit<N>(gb, ub, a, ag, au);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const float s = b < p.nb && j < n ? sc[slots[min(j, n - 1)] * 4 * p.nq + b] : 0.0f;
-            float x = b < p.nb ? joined(ag[j]) * (dg * s) : 0.0f, y = b < p.nb ? joined(au[j]) * (du * s) : 0.0f;
+            float x = b < p.nb ? joined(ag[j]) * (gb.d * s) : 0.0f, y = b < p.nb ? joined(au[j]) * (ub.d * s) : 0.0f;
             x = sum_rows(x);
             y = sum_rows(y);
             if (g < 2) red[(u * N + j) * 32 + lane] = g ? y : x;
         }
-    }
+    };
+    Pair next;
+    load(wave, next);
+    for (int u = wave; u < units; u += NW) unit(u, next);
     __syncthreads();
     // a wave finishes 64 features of a token: SwiGLU, digits, sums
     const int groups = p.F / 64;
@@ -599,14 +587,13 @@ __device__ __noinline__ void routed_units(Args pa, int e, int f0, int n)
     }
 }
 
-__device__ __noinline__ void routed_item(Args pa, int item)
+__device__ __forceinline__ void routed_item(const BlockPass &p, Args pa, int item)
 {
-    const BlockPass &p = args_of(pa);
     auto &now = small().routed;
     const int d = item / p.nf, f0 = item % p.nf * p.F;
     const int entry = small().entry[d], e = entry & 1023, first = entry >> 10 & 1023, n = entry >> 20;
-    for (int j0 = 0; j0 < n; j0 += 4) {
-        const int m = min(4, n - j0);
+    for (int j0 = 0; j0 < n; j0 += 2) {
+        const int m = min(2, n - j0);
         __syncthreads();
         if (threadIdx.x < m) {
             const int i = threadIdx.x, t = small().tok[first + j0 + i];
@@ -619,9 +606,8 @@ __device__ __noinline__ void routed_item(Args pa, int item)
             stage_tokens(pa, 0, now.token, m);
             __syncthreads();
         }
-        if (m == 1) routed_units<1>(pa, e, f0, m);
-        else if (m == 2) routed_units<2>(pa, e, f0, m);
-        else routed_units<4>(pa, e, f0, m);
+        if (m == 1) routed_units<1>(p, e, f0, m);
+        else routed_units<2>(p, e, f0, m);
     }
 }
 
@@ -733,11 +719,11 @@ __device__ __forceinline__ bool down_items(const BlockPass &p, int item, int bas
     bool first = true;                           // the waits are still to come
     while (item < p.t_down) {
         const int r0 = item * p.rows;
-        auto load_down = [&](int v, int lo) {    // unit v: expert lo + v / units, quad of blocks, tile
+        auto load_down = [&](int v, int lo, int total, DownBlock &x) { // unit v: expert lo + v / units, quad of blocks, tile
+            if (v >= total) return;
             const int u = v % units, e = small().entry[lo + v / units] & 1023;
             const int row = min(r0 + u % tiles * 16 + r, p.H - 1), b = min(4 * (u / tiles) + g, p.nbi - 1);
             const uint32_t *const at = (const uint32_t *)(p.down + (((int64_t)e * p.H + row) * p.nbi + b) * 84);
-            DownBlock x;
 #pragma unroll
             for (int i = 0; i < 5; ++i) {
                 const u32x4u q = *(const u32x4u *)(at + 4 * i);
@@ -745,19 +731,24 @@ __device__ __forceinline__ bool down_items(const BlockPass &p, int item, int bas
                 for (int j = 0; j < 4; ++j) x.c[4 * i + j] = q[j];
             }
             x.c[20] = at[20];
-            return x;
         };
         for (int i = lane; i < p.T * 32; i += 64) ya[i] = 0.0f;
+        int count = min(p.chunk, n), lo = 0, total = (small().seg[count - 1] + 1) * units;
+        DownBlock even, odd;
         if (p.sh) {
-            i32x4 w[4];
-            float ws = 0.0f;
-            auto load_shared = [&](int u) {      // unit u: tile, block
+            struct Rows { i32x4 w[4]; float scale; };
+            auto load_shared = [&](int u, Rows &x) {                   // unit u: tile, block
+                if (u >= tiles * p.nbs) return;
                 const int row = min(r0 + u % tiles * 16 + r, p.H - 1);
-                ws = p.down_scale[row];
+                x.scale = p.down_scale[row];
 #pragma unroll
-                for (int s = 0; s < 4; ++s) w[s] = load_row16(p.sh_down + (int64_t)row * p.ld_down, 256 * (u / tiles) + 64 * s + 16 * g, p.sh);
+                for (int s = 0; s < 4; ++s) x.w[s] = load_row16(p.sh_down + (int64_t)row * p.ld_down, 256 * (u / tiles) + 64 * s + 16 * g, p.sh);
             };
-            if (wave < tiles * p.nbs) load_shared(wave);
+            Rows x0, x1;
+            load_shared(wave, x0);
+            load_shared(wave + NW, x1);
+            load_down(wave, lo, total, even);
+            load_down(wave + NW, lo, total, odd);
             if (first) {
                 if (tid == 0) word = wait_for(p.ctl + C_SHARED, (uint32_t)p.t_shared);
                 __syncthreads();
@@ -770,8 +761,7 @@ __device__ __forceinline__ bool down_items(const BlockPass &p, int item, int bas
                 stage_shared(p, t0, nt);
                 __syncthreads();
                 const float *const sc = (const float *)(smem + p.o_planes + nt * p.nqs * QUAD);
-                for (int u = wave; u < tiles * p.nbs; u += NW) {
-                    if (u != wave || t0) load_shared(u);
+                auto unit = [&](int u, const Rows &x) {
                     const int tile = u % tiles, b = u / tiles;
                     for (int tg = 0; tg < nt; tg += 4) {
                         const int slot = tg + (r >> 2), digit = r & 3, tt = tg + g;
@@ -780,18 +770,33 @@ __device__ __forceinline__ bool down_items(const BlockPass &p, int item, int bas
                             digit_base(p, in, slot, p.nqs * QUAD, (b >> 2) * QUAD + g * 192 + ((b & 3) * 3 + digit) * 16);
                         i32x4 acc = {0, 0, 0, 0};
 #pragma unroll
-                        for (int s = 0; s < 4; ++s) acc = mfma_i8(*(const i32x4 *)(a + s * 768), w[s], acc);
-                        if (tt < nt) ya[(t0 + tt) * 32 + tile * 16 + r] += joined(acc) * (sc[tt * 4 * p.nqs + b] * ws);
+                        for (int s = 0; s < 4; ++s) acc = mfma_i8(*(const i32x4 *)(a + s * 768), x.w[s], acc);
+                        if (tt < nt) ya[(t0 + tt) * 32 + tile * 16 + r] += joined(acc) * (sc[tt * 4 * p.nqs + b] * x.scale);
                     }
+                };
+                if (t0) {
+                    load_shared(wave, x0);
+                    load_shared(wave + NW, x1);
+                }
+                for (int u = wave; u < tiles * p.nbs; u += 2 * NW) {
+                    unit(u, x0);
+                    load_shared(u + 2 * NW, x0);
+                    if (u + NW < tiles * p.nbs) unit(u + NW, x1);
+                    load_shared(u + 3 * NW, x1);
                 }
             }
+        } else {
+            load_down(wave, lo, total, even);
+            load_down(wave + NW, lo, total, odd);
         }
         for (int c0 = 0; c0 < n; c0 += p.chunk) {
-            const int count = min(p.chunk, n - c0);
-            const int lo = small().seg[c0], total = (small().seg[c0 + count - 1] + 1 - lo) * units;
-            DownBlock x, x1;
-            if (wave < total) x = load_down(wave, lo);
-            if (wave + NW < total) x1 = load_down(wave + NW, lo);
+            if (c0) {
+                count = min(p.chunk, n - c0);
+                lo = small().seg[c0];
+                total = (small().seg[c0 + count - 1] + 1 - lo) * units;
+                load_down(wave, lo, total, even);
+                load_down(wave + NW, lo, total, odd);
+            }
             if (first) {
                 if (tid == 0) word = wait_for(p.ctl + C_ROUTED, (uint32_t)(n_list * p.nf));
                 __syncthreads();
@@ -801,7 +806,10 @@ __device__ __forceinline__ bool down_items(const BlockPass &p, int item, int bas
             __syncthreads();
             stage_h(p, c0, count);
             __syncthreads();
-            auto unit = [&](int v, const DownBlock &now) {
+            // a unit's blocks are requested two units ahead
+            auto unit = [&](int v, DownBlock &x) {
+                const DownBlock now = x;
+                load_down(v + 2 * NW, lo, total, x);
                 const int u = v % units, tile = u % tiles, quad = u / tiles, entry = small().entry[lo + v / units];
                 const int begin = max(entry >> 10 & 1023, c0), end = min((entry >> 10 & 1023) + (entry >> 20), c0 + count);
                 for (int j = begin; j < end; j += 2) {
@@ -810,10 +818,8 @@ __device__ __forceinline__ bool down_items(const BlockPass &p, int item, int bas
                 }
             };
             for (int v = wave; v < total; v += 2 * NW) {
-                unit(v, x);
-                if (v + 2 * NW < total) x = load_down(v + 2 * NW, lo);
-                if (v + NW < total) unit(v + NW, x1);
-                if (v + 3 * NW < total) x1 = load_down(v + 3 * NW, lo);
+                unit(v, even);
+                if (v + NW < total) unit(v + NW, odd);
             }
         }
         __syncthreads();
@@ -838,16 +844,16 @@ __device__ __forceinline__ bool down_items(const BlockPass &p, int item, int bas
     return true;
 }
 
-// selectors of the codewords, 16 copies (a lane reads copy lane % 16: no two of 16 lanes share a bank), and the zeros
+// the codewords, 16 copies (a lane reads copy lane % 16: no two of 16 lanes share a bank), and the zeros
 __device__ __noinline__ void tables(Args pa)
 {
     const BlockPass &p = args_of(pa);
-    for (int i = threadIdx.x; i < 4096; i += NT) {
-        const uint2 c = *(const uint2 *)(p.codebook + 8 * (i >> 4));
-        // (C + 3) / 2 of bytes -3, -1, 1, 3, added without a carry into the next byte
-        auto code = [](uint32_t v) { return (((v & 0x7f7f7f7fu) + 0x03030303u) ^ (v & 0x80808080u)) >> 1 & 0x03030303u; };
-        *(uint2 *)(smem + 8 * i) = uint2{code(c.x), code(c.y)};
-    }
+    static_assert(NT == 512, "two threads a codeword");
+    const int i = threadIdx.x >> 1;
+    const uint2 c = *(const uint2 *)(p.codebook + 8 * i);
+    const u32x4 two = {c.x, c.y, c.x, c.y};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *(u32x4 *)(smem + 128 * i + 64 * (threadIdx.x & 1) + 16 * j) = two;
     for (int i = threadIdx.x; i < QUAD / 4; i += NT) ((uint32_t *)(smem + O_ZERO))[i] = 0;
 }
 
@@ -885,7 +891,7 @@ __global__ __launch_bounds__(NT) void block_kernel(BlockPass p)
     if (tid == 0) next = draw(ctl);
     tables(pa);
     bool resident = false;                       // all tokens' digits are in LDS
-    int n_list = -1, base = 0, item;
+    int item;
     for (;;) {
         __syncthreads();
         item = (int)next;
@@ -911,24 +917,27 @@ __global__ __launch_bounds__(NT) void block_kernel(BlockPass p)
             arrive(ctl, C_SHARED, next);
             continue;
         }
-        if (n_list < 0) {
-            if (!resident && p.T <= p.slots) {
-                stage_tokens(pa, 0, nullptr, p.T);
-                resident = true;
-            }
-            if (tid == 0) word = wait_for(ctl + C_LIST, 1) ? peek(ctl + C_LIST) : 0;
-            __syncthreads();
-            n_list = (int)word;
-            if (n_list == 0) break;
-            load_list(pa, n_list);
-            base = 1 + p.t_shared + n_list * p.nf;
-        }
-        item -= p.t_shared;
-        if (item >= n_list * p.nf) break;
-        routed_item(pa, item);
-        arrive(ctl, C_ROUTED, next);
+        break;
     }
-    if (n_list == 0 || !down_items(p, item - n_list * p.nf, base, n_list, next, word)) give_up(pa);
+    // the rest is inlined: it needs all registers, and would save and restore them at every call
+    item -= p.t_shared;
+    if (!resident && p.T <= p.slots) stage_tokens(pa, 0, nullptr, p.T);
+    if (tid == 0) word = wait_for(ctl + C_LIST, 1) ? peek(ctl + C_LIST) : 0;
+    __syncthreads();
+    const int n_list = (int)word, n_routed = n_list * p.nf;
+    if (n_list == 0) {
+        give_up(pa);
+        return;
+    }
+    load_list(pa, n_list);
+    while (item < n_routed) {
+        routed_item(p, pa, item);
+        arrive(ctl, C_ROUTED, next);
+        __syncthreads();
+        item = (int)next - 1 - p.t_shared;
+        __syncthreads();
+    }
+    if (!down_items(p, item - n_routed, 1 + p.t_shared + n_routed, n_list, next, word)) give_up(pa);
 }
 
 }  // namespace
@@ -950,7 +959,7 @@ void block_layout(BlockPass &p)
     p.slots = std::min(p.T, 4);
     // LDS: table, zeros, planes (or rows of h), scales, sums
     const int units = p.F / 16 * p.nq;
-    const int sums = std::max({units * (p.slots <= 2 ? p.slots : 4) * 128, NW * 64 * 4, NW * p.T * 128});
+    const int sums = std::max({units * std::min(p.slots, 2) * 128, NW * 64 * 4, NW * p.T * 128});
     const int red = sums + NW * REC;             // and the waves' records
     const int scales = p.slots * 4 * p.nq * 4;
     const int row_i = p.nqi * 4 * REC_BLOCK, row_s = p.nqs * (QUAD + 16), row = std::max(row_i, row_s);
