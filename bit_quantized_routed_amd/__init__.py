@@ -27,6 +27,7 @@ LAYER_ONE_STREAM = 2
 SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
 ROUTER_RENORM = 1
 Q8_SWIGLU = 1
+ADAPT_F32, ADAPT_BF16, ADAPT_I8 = 0, 1, 2
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED",
           -3: "MOE_ERR_WORKSPACE", -4: "MOE_ERR_HIP"}
 BLOCK_BYTES = {FMT_CB2: 38, FMT_Q2K: 84, FMT_Q4K: 144, FMT_Q5K: 176, FMT_Q6K: 210, FMT_CB2S: 66}
@@ -86,6 +87,13 @@ class BlockC(ctypes.Structure):
                 ("gate_up", ctypes.POINTER(LinearC)), ("down", ctypes.POINTER(LinearC)), ("act_n", ctypes.c_int32)]
 
 
+class AdapterSetC(ctypes.Structure):
+    """struct moe_adapter_set (host struct of device pointers)."""
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("n_adapters", ctypes.c_int32),
+                ("rank", ctypes.c_int32), ("parts", ctypes.c_int32), ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64),
+                ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
 class Profile(ctypes.Structure):
     """struct moe_profile: bracket launch number `kernel` with two hipEvents."""
     _fields_ = [("kernel", ctypes.c_int32), ("n_launches", ctypes.c_int32),
@@ -100,7 +108,8 @@ EXPORTS = ["moe_route", "moe_expert_ffn_decode", "moe_expert_ffn_prefill", "q2_p
            "moe_expert_ffn_decode_noalloc", "moe_layer_decode", "moe_expert_cache_bytes", "moe_expert_cache_init",
            "moe_expert_cache_map", "moe_expert_cache_prefetch", "moe_route_scored", "moe_route_scored_workspace_bytes",
            "moe_residual_norm", "moe_quant_i8", "moe_linear_i8", "moe_linear_i8_workspace_bytes",
-           "moe_block_decode", "moe_block_decode_workspace_bytes"]
+           "moe_block_decode", "moe_block_decode_workspace_bytes", "moe_adapter_tiles", "moe_adapter_plan", "moe_adapters",
+           "moe_adapters_workspace_bytes"]
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 # measurement kernels the benchmark uses (csrc/moe_probe.h; not part of the layer's ABI)
 PROBE_EXPORTS = ["moe_probe_stream_read", "moe_probe_mfma_loop"]
@@ -164,6 +173,15 @@ def lib():
     L.moe_block_decode.restype = i32
     L.moe_block_decode_workspace_bytes.argtypes = [bp, i32]
     L.moe_block_decode_workspace_bytes.restype = sz
+    ap = ctypes.POINTER(AdapterSetC)
+    L.moe_adapter_tiles.argtypes = [i32, i32]
+    L.moe_adapter_tiles.restype = i32
+    L.moe_adapter_plan.argtypes = [vp, i32, i32, vp, vp, vp, vp, pp]
+    L.moe_adapter_plan.restype = i32
+    L.moe_adapters.argtypes = [ap, i32, vp, vp, vp, vp, i32, i64, vp, vp, i64, vp, i32, i64, vp, sz, vp, pp]
+    L.moe_adapters.restype = i32
+    L.moe_adapters_workspace_bytes.argtypes = [ap, i32]
+    L.moe_adapters_workspace_bytes.restype = sz
     L.moe_probe_stream_read.argtypes = [vp, sz, i32, i32, vp, vp]
     L.moe_probe_stream_read.restype = i32
     L.moe_probe_mfma_loop.argtypes = [i32, i32, i32, vp, vp]
@@ -630,3 +648,85 @@ def block_decode(w: BlockWeights, x, residual, total, y, r: Routing, ws, stream=
                                             r.topk_idx.data_ptr(), r.topk_w.data_ptr(), r.offsets.data_ptr(),
                                             r.perm.data_ptr(), r.inv.data_ptr(), ws.data_ptr(), ws.nbytes, _stream(stream),
                                             None if prof is None else ctypes.byref(prof)), "moe_block_decode")
+
+
+# ------------------------------------------------------------------ low-rank adapters
+class AdapterWeights:
+    """The adapters beside one projection: a [n, parts * rank, in_features], b [n, out_features, rank] (bf16), scale [n] (fp32).
+    Copies a and b where their rows are no multiple of 16 bytes."""
+
+    def __init__(self, a, b, scale, parts: int = 1):
+        import torch
+        n, width, K = a.shape
+        _, N, r = b.shape
+        if a.dtype != torch.bfloat16 or b.dtype != torch.bfloat16 or b.shape[0] != n or width != parts * r:
+            raise ValueError("adapters: a [n, parts * rank, in] and b [n, out, rank] in bf16 are needed, got %s %s and %s %s, parts %d"
+                             % (a.dtype, tuple(a.shape), b.dtype, tuple(b.shape), parts))
+        self.a, self.b, self.scale = self._rows(a), self._rows(b), _vector(scale, n, "scale")
+        self.in_features, self.out_features, self.n_adapters, self.rank, self.parts = K, N, n, r, parts
+        self.c = AdapterSetC(K, N, n, r, parts, self.a.stride(1), self.b.stride(1), _ptr(self.a), _ptr(self.b), _ptr(scale))
+        self.ref = ctypes.byref(self.c)
+
+    @staticmethod
+    def _rows(t):
+        import torch
+        n, rows, k = t.shape
+        if k % 8 == 0 and t.is_contiguous() and t.data_ptr() % 16 == 0:
+            return t
+        out = torch.zeros((n, rows, (k + 7) // 8 * 8), dtype=t.dtype, device=t.device)
+        out[:, :, :k] = t
+        return out
+
+    def workspace(self, T: int, device="cuda"):
+        """A workspace for up to T tokens."""
+        import torch
+        n = int(lib().moe_adapters_workspace_bytes(self.ref, T))
+        if n == 0 and T:
+            raise ValueError("no workspace for %d tokens: %s" % (T, lib().moe_last_error().decode()))
+        return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+class AdapterPlan:
+    """Buffers of the plan for T tokens of n_adapters adapters (see adapter_plan)."""
+
+    def __init__(self, T: int, n_adapters: int, device="cuda"):
+        import torch
+        i32 = dict(dtype=torch.int32, device=device)
+        tiles = int(lib().moe_adapter_tiles(T, n_adapters))
+        if T and tiles == 0:
+            raise ValueError("no plan for %d tokens of %d adapters" % (T, n_adapters))
+        self.T, self.n_adapters = T, n_adapters
+        self.order, self.offsets, self.tiles = torch.empty(T, **i32), torch.empty(n_adapters + 1, **i32), torch.empty((tiles, 2), **i32)
+
+
+def adapter_plan(ids, plan: AdapterPlan, stream=None, prof=None):
+    """Sorts the tokens by the adapter in ids (int32 [T]; outside [0, n_adapters): none), for every projection of a step."""
+    import torch
+    if ids.dtype != torch.int32 or ids.shape != (plan.T,) or not ids.is_contiguous():
+        raise ValueError("ids: %d contiguous int32 values are needed" % plan.T)
+    _check((_lib or lib()).moe_adapter_plan(ids.data_ptr(), plan.T, plan.n_adapters, plan.order.data_ptr(), plan.offsets.data_ptr(),
+                                            plan.tiles.data_ptr(), _stream(stream), None if prof is None else ctypes.byref(prof)),
+           "moe_adapter_plan")
+
+
+def adapters(w: AdapterWeights, plan: AdapterPlan, x, x_scale, y, add=None, ws=None, stream=None, prof=None):
+    """y = add + scale B (A x) by each token's adapter; x in fp32 or bf16, or int8 codes with x_scale; add: y itself if None."""
+    T = plan.T
+    if plan.n_adapters != w.n_adapters:
+        raise ValueError("plan of %d adapters, weights of %d" % (plan.n_adapters, w.n_adapters))
+    if x_scale is None:
+        kind, ldx = _rows(x, T, w.in_features, "x")
+    else:
+        kind, ldx = ADAPT_I8, _codes(x, T, w.in_features, "x")
+        x_scale = _vector(x_scale, T, "x_scale").data_ptr()
+    act, ldy = _rows(y, T, w.out_features, "y")
+    pa, lda = y.data_ptr(), ldy
+    if add is not None:
+        aa, lda = _rows(add, T, w.out_features, "add")
+        if aa != act:
+            raise ValueError("add: y's type is needed")
+        pa = add.data_ptr()
+    _check((_lib or lib()).moe_adapters(w.ref, T, plan.order.data_ptr(), plan.offsets.data_ptr(), plan.tiles.data_ptr(), x.data_ptr(),
+                                        kind, ldx, x_scale, pa, lda, y.data_ptr(), act, ldy,
+                                        *((None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)), _stream(stream),
+                                        None if prof is None else ctypes.byref(prof)), "moe_adapters")

@@ -3,6 +3,7 @@
 // validation and the launch sequences.
 #include <hip/hip_runtime.h>
 
+#include "adapters.h"
 #include "block.h"
 #include "dense_check.h"
 #include "linear.h"
@@ -83,6 +84,24 @@ int check_block(const moe_block *B, int T, BlockPass &p)
     r.T = T; r.H = H; r.E = E; r.k = k;
     r.softmax = R->score == MOE_SCORE_SOFTMAX; r.groups = R->n_groups; r.keep = R->keep_groups;
     r.renorm = (R->flags & MOE_ROUTER_RENORM) != 0; r.scale = R->scale; r.w = R->w_router; r.bias = R->bias;
+    return MOE_OK;
+}
+
+int check_adapters(const moe_adapter_set *W)
+{
+    if (!W) return set_error(MOE_ERR_INVALID_ARG, "adapter set is NULL");
+    if (W->in_features < 1 || W->in_features > (1 << 24)) return set_error(MOE_ERR_INVALID_ARG, "in_features=%d outside [1,2^24]", W->in_features);
+    if (W->out_features < 1 || W->out_features > (1 << 24)) return set_error(MOE_ERR_INVALID_ARG, "out_features=%d outside [1,2^24]", W->out_features);
+    if (W->n_adapters < 1 || W->n_adapters > ADAPT_MAX) return set_error(MOE_ERR_INVALID_ARG, "n_adapters=%d outside [1,%d]", W->n_adapters, ADAPT_MAX);
+    if (W->rank < 1 || W->rank > ADAPT_MAX_RANK) return set_error(MOE_ERR_INVALID_ARG, "rank=%d outside [1,%d]", W->rank, ADAPT_MAX_RANK);
+    if (W->parts < 1 || W->out_features % W->parts || W->parts > ADAPT_MAX_WIDTH / W->rank)
+        return set_error(MOE_ERR_INVALID_ARG, "parts=%d: not a divisor of out_features=%d, or parts * rank > %d", W->parts, W->out_features, ADAPT_MAX_WIDTH);
+    if (!W->a || !W->b || !W->scale) return set_error(MOE_ERR_INVALID_ARG, "adapter weights are NULL");
+    if (((uintptr_t)W->a | (uintptr_t)W->b) % 16 || (uintptr_t)W->scale % 4)
+        return set_error(MOE_ERR_INVALID_ARG, "a and b must be 16-byte and scale 4-byte aligned");
+    if (W->lda % 8 || W->lda < W->in_features || W->ldb % 8 || W->ldb < W->rank || W->lda > ((int64_t)1 << 40) || W->ldb > ((int64_t)1 << 40))
+        return set_error(MOE_ERR_INVALID_ARG, "lda=%lld and ldb=%lld must be multiples of 8 of at least in_features and rank", (long long)W->lda,
+                         (long long)W->ldb);
     return MOE_OK;
 }
 
@@ -295,6 +314,69 @@ int moe_block_decode(const moe_block *B, int T, const void *x, int act_x, int64_
     Launcher run{prof, s};
     if ((rc = run("block_norm", [&] { return launch_block_norm(p, s); }))) return rc;
     return run("block", [&] { return launch_block(p, s); });
+}
+
+int moe_adapter_tiles(int T, int n_adapters)
+{
+    return T < 1 || T > ADAPT_MAX_T || n_adapters < 1 || n_adapters > ADAPT_MAX ? 0 : adapter_tiles(T, n_adapters);
+}
+
+int moe_adapter_plan(const int32_t *ids, int T, int n_adapters, int32_t *order, int32_t *offsets, int32_t *tiles, void *stream,
+                     moe_profile *prof)
+{
+    if (T < 0) return set_error(MOE_ERR_INVALID_ARG, "T=%d < 0", T);
+    if (n_adapters < 1 || n_adapters > ADAPT_MAX) return set_error(MOE_ERR_INVALID_ARG, "n_adapters=%d outside [1,%d]", n_adapters, ADAPT_MAX);
+    if (prof) prof->n_launches = 0;
+    if (T == 0) return MOE_OK;
+    if (T > ADAPT_MAX_T) return set_error(MOE_ERR_UNSUPPORTED, "T=%d: more tokens than one plan takes", T);
+    if (!ids || !order || !offsets || !tiles) return set_error(MOE_ERR_INVALID_ARG, "NULL tensor argument");
+    if (((uintptr_t)ids | (uintptr_t)order | (uintptr_t)offsets) % 4 || (uintptr_t)tiles % 8)
+        return set_error(MOE_ERR_INVALID_ARG, "ids, order and offsets must be 4-byte, tiles 8-byte aligned");
+    Launcher run{prof, (hipStream_t)stream};
+    return run("adapter_plan", [&] {
+        return launch_adapter_plan(ids, T, n_adapters, order, offsets, (AdapterTile *)tiles, (hipStream_t)stream);
+    });
+}
+
+size_t moe_adapters_workspace_bytes(const moe_adapter_set *W, int T)
+{
+    if (T < 0 || T > ADAPT_MAX_T || check_adapters(W)) return 0;
+    return align_up(adapter_low_bytes(T, W->in_features, W->parts * W->rank, W->n_adapters));
+}
+
+int moe_adapters(const moe_adapter_set *W, int T, const int32_t *order, const int32_t *offsets, const int32_t *tiles,
+                 const void *x, int kind_x, int64_t ldx, const float *x_scale, const void *add, int64_t ldadd, void *y,
+                 int act_y, int64_t ldy, void *ws, size_t ws_bytes, void *stream, moe_profile *prof)
+{
+    int rc = check_adapters(W);
+    if (rc) return rc;
+    if (T < 0) return set_error(MOE_ERR_INVALID_ARG, "T=%d < 0", T);
+    if (kind_x != MOE_ADAPT_F32 && kind_x != MOE_ADAPT_BF16 && kind_x != MOE_ADAPT_I8) return set_error(MOE_ERR_INVALID_ARG, "kind_x=%d unknown", kind_x);
+    if (!act_ok(act_y)) return set_error(MOE_ERR_INVALID_ARG, "act_y=%d unknown", act_y);
+    if (prof) prof->n_launches = 0;
+    if (T == 0) return MOE_OK;
+    if (T > ADAPT_MAX_T) return set_error(MOE_ERR_UNSUPPORTED, "T=%d: more tokens than one plan takes", T);
+    if (!order || !offsets || !tiles) return set_error(MOE_ERR_INVALID_ARG, "the plan is NULL");
+    if (((uintptr_t)order | (uintptr_t)offsets) % 4 || (uintptr_t)tiles % 8) return set_error(MOE_ERR_INVALID_ARG, "the plan is not aligned");
+    if ((rc = check_rows("x", x, ldx, T, W->in_features, kind_x == MOE_ADAPT_F32 ? 4 : kind_x == MOE_ADAPT_BF16 ? 2 : 1))) return rc;
+    if (!x_scale != (kind_x != MOE_ADAPT_I8) || (uintptr_t)x_scale % 4)
+        return set_error(MOE_ERR_INVALID_ARG, "x_scale comes with codes, and only with them, 4-byte aligned");
+    if ((rc = check_rows("y", y, ldy, T, W->out_features, act_size(act_y)))) return rc;
+    if ((rc = check_rows("add", add, ldadd, T, W->out_features, act_size(act_y)))) return rc;
+    const size_t need = (size_t)adapter_k_parts(T, W->in_features, W->n_adapters) * T * W->parts * W->rank * sizeof(float);
+    if (!ws || (uintptr_t)ws % 16) return set_error(MOE_ERR_INVALID_ARG, "the workspace is NULL or not 16-byte aligned");
+    if (ws_bytes < need) return set_error(MOE_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+    AdapterPass p{};
+    p.T = T; p.K = W->in_features; p.N = W->out_features; p.n = W->n_adapters; p.rank = W->rank; p.parts = W->parts;
+    p.kind = kind_x == MOE_ADAPT_F32 ? ADAPT_F32 : kind_x == MOE_ADAPT_BF16 ? ADAPT_BF16 : ADAPT_I8;
+    p.x = x; p.x_scale = x_scale; p.ldx = ldx;
+    p.a = (const uint16_t *)W->a; p.b = (const uint16_t *)W->b; p.lda = W->lda; p.ldb = W->ldb; p.scale = W->scale;
+    p.add = add; p.ldadd = ldadd; p.y = y; p.ldy = ldy; p.y_bf16 = act_y == MOE_ACT_BF16;
+    p.order = order; p.offsets = offsets; p.tiles = (const AdapterTile *)tiles; p.low = (float *)ws;
+    const hipStream_t s = (hipStream_t)stream;
+    Launcher run{prof, s};
+    if ((rc = run("adapter_down", [&] { return launch_adapter_down(p, s); }))) return rc;
+    return run("adapter_up", [&] { return launch_adapter_up(p, s); });
 }
 
 }  // extern "C"

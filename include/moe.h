@@ -508,6 +508,45 @@ int moe_block_decode(const moe_block *B, int T, const void *x, int act_x, int64_
                      moe_profile *prof);
 size_t moe_block_decode_workspace_bytes(const moe_block *B, int T);
 
+/* ------------------------------------------------------------ low-rank adapters
+ * The adapters of many requests beside one projection (a linear layer of `parts` equal
+ * parts of its outputs, as [gate | up] has two), each token with its own or none:
+ *     low[t, q r + j] = sum_k x[t, k] * A_a[q r + j, k]                      (fp32 sums)
+ *     y[t, n] = add[t, n] + scale_a * sum_j low[t, q r + j] * B_a[n, j]      q = n / (out_features / parts)
+ * with a = ids[t] and r = rank; the whole sum is rounded once to y's type.
+ * moe_adapter_plan: sorts a batch's tokens by adapter (stable), once for all the
+ *   projections of a step.  ids [T] (device int32); an id outside [0, n_adapters) means no
+ *   adapter.  order [T]: the tokens sorted, those without an adapter last; offsets
+ *   [n_adapters + 1]: adapter a's tokens are order[offsets[a] .. offsets[a + 1]); tiles
+ *   [moe_adapter_tiles(T, n_adapters)] pairs of int32: for moe_adapters.  T <= 2^20
+ *   (MOE_ERR_UNSUPPORTED otherwise), 1 <= n_adapters <= 1024.
+ * moe_adapters: x [T] rows of type MOE_ADAPT_F32, BF16 or I8 (codes, x_scale [T] then, else
+ *   NULL); y and add [T] rows of type act_y (add may be y).  Where a token has no adapter, y
+ *   is add, bit for bit.  The plan's three arrays are those of the same T and n_adapters.
+ *   a: bf16 [n][parts * rank] rows lda elements apart, b: bf16 [n][out_features] rows ldb
+ *   apart, both 16-byte aligned with lda and ldb multiples of 8; elements past in_features
+ *   and rank up to the next multiple of 8 are read and must be zero.  scale: fp32 [n].
+ *   1 <= rank <= 64, parts divides out_features, parts * rank <= 256.  An adapter of a
+ *   smaller rank has zeros in the rest.  x, y and add: element-aligned, strides in elements;
+ *   rows of 16-byte aligned pieces run fastest.  fp32 inputs go as three bf16 terms that add
+ *   up to them, products and terms are exact; values past 3.38e38 or infinite give NaN.
+ *   Workspace: moe_adapters_workspace_bytes() (0 if W is invalid), for every batch of up to T
+ *   tokens, 16-byte aligned, no clearing. */
+enum moe_adapt_x { MOE_ADAPT_F32 = 0, MOE_ADAPT_BF16 = 1, MOE_ADAPT_I8 = 2 };
+typedef struct moe_adapter_set {
+    int32_t in_features, out_features, n_adapters, rank, parts;
+    int64_t lda, ldb;
+    const void *a, *b;
+    const float *scale;
+} moe_adapter_set;
+int moe_adapter_tiles(int T, int n_adapters);
+int moe_adapter_plan(const int32_t *ids, int T, int n_adapters, int32_t *order, int32_t *offsets, int32_t *tiles, void *stream,
+                     moe_profile *prof);
+int moe_adapters(const moe_adapter_set *W, int T, const int32_t *order, const int32_t *offsets, const int32_t *tiles,
+                 const void *x, int kind_x, int64_t ldx, const float *x_scale, const void *add, int64_t ldadd, void *y,
+                 int act_y, int64_t ldy, void *ws, size_t ws_bytes, void *stream, moe_profile *prof);
+size_t moe_adapters_workspace_bytes(const moe_adapter_set *W, int T);
+
 /* ------------------------------------------------------------ pack / unpack
  * q2_pack (host): quantize a row-major fp32 matrix w_host [rows][K] into
  * out_host (q2_packed_bytes(fmt, rows, K) bytes).  fmt: CB2 (needs
