@@ -24,7 +24,7 @@ struct AdapterPass {
     int y_bf16;
     const int32_t *order, *offsets;
     const AdapterTile *tiles;
-    float *low;                                  // workspace: [parts of K][T, in the plan's order][parts * rank]
+    float *low;                                  // workspace: [parts of K][T, in the plan's order][parts][rank up to a multiple of 8]
 };
 
 inline int adapter_tile(int T) { return T <= 512 ? 16 : 64; }

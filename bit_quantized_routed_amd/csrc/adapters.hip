@@ -209,18 +209,21 @@ __device__ __forceinline__ void as_terms(const Raw &v, bf16x8 t[3])
 }
 
 // ---------------------------------------------------------------- down: low = x A^T
-// A work-group takes a tile (TT fragments of 16 tokens) and one part of K.  Its four
-// waves share out the columns of low (CW ways) and what is left of the split the
-// steps of 32 of K; these sums meet in LDS in a fixed order.
-template <int TT, int KIND, bool VEC>
-__global__ __launch_bounds__(256) void adapter_down(AdapterPass p, int k_parts, int cw)
+// A work-group takes a tile (TT fragments of 16 tokens) and one part of K.  Its eight
+// waves share out the columns of low (cw ways, up to CT fragments each) and what is
+// left of the split the steps of 32 of K; these sums meet in LDS in a fixed order.
+constexpr int NW = 8;
+
+template <int TT, int CT, int KIND, bool VEC>
+__global__ __launch_bounds__(64 * NW) void adapter_down(AdapterPass p, int k_parts, int cw)
 {
-    constexpr int NS = terms<KIND>(), CT = ADAPT_MAX_WIDTH / 64;       // column fragments of a wave at most
+    constexpr int NS = terms<KIND>();
     const AdapterTile tile = p.tiles[blockIdx.x];
     if (tile.adapter < 0) return;
     const int end = p.offsets[tile.adapter + 1], count = min(16 * TT, end - tile.begin);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-    const int R = p.parts * p.rank, frags = (R + 15) / 16, kw = 4 / cw, wc = wave % cw, wk = wave / cw;
+    const int R = p.parts * p.rank, frags = (R + 15) / 16, kw = NW / cw, wc = wave % cw, wk = wave / cw;
+    const int r8 = (p.rank + 7) & ~7, width = p.parts * r8;
     const int steps = (p.K + 31) / 32, part = blockIdx.y;
     const int s0 = (int)((int64_t)steps * part / k_parts), s1 = (int)((int64_t)steps * (part + 1) / k_parts);
     const void *row[TT];
@@ -272,145 +275,181 @@ __global__ __launch_bounds__(256) void adapter_down(AdapterPass p, int k_parts, 
                         acc[i][c] = mfma16x16x32(a[i][q], __builtin_bit_cast(bf16x8, b[c]), acc[i][c]);
             }
     }
-    extern __shared__ f32x4 sums[];              // [kw - 1][TT][column fragments][64]
-    if (wk > 0) {
+    // sums over the waves that share these columns, by halves
+    extern __shared__ f32x4 sums[];              // [kw / 2][TT][column fragments][64]
+    for (int half = kw / 2; half > 0; half /= 2) {
+        f32x4 *const at = sums + ((wk & (half - 1)) * TT * frags + wc) * 64 + lane;
+        if (wk >= half && wk < 2 * half) {
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
-            if (c < n_cols) {
+            for (int c = 0; c < CT; ++c)
+                if (c < n_cols) {
 #pragma unroll
-                for (int i = 0; i < TT; ++i) sums[((wk - 1) * TT + i) * frags * 64 + (wc + c * cw) * 64 + lane] = acc[i][c];
-            }
+                    for (int i = 0; i < TT; ++i) at[(i * frags + c * cw) * 64] = acc[i][c];
+                }
+        }
+        __syncthreads();
+        if (wk < half) {
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+                if (c < n_cols) {
+#pragma unroll
+                    for (int i = 0; i < TT; ++i) acc[i][c] += at[(i * frags + c * cw) * 64];
+                }
+        }
+        __syncthreads();
     }
-    if (kw > 1) __syncthreads();
     if (wk > 0) return;
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
-        if (c < n_cols) {
-            const int f = wc + c * cw;
+    for (int c = 0; c < CT; ++c) {
+        const int f = 16 * (wc + c * cw) + r;    // D: lane (r, g) holds tokens 4 g .. 4 g + 3 of column r
+        if (c >= n_cols || f >= R) continue;
+        float *const o = p.low + ((int64_t)part * p.T + tile.begin) * width + f / p.rank * r8 + f % p.rank;
 #pragma unroll
-            for (int i = 0; i < TT; ++i) {
-                for (int k = 1; k < kw; ++k) acc[i][c] += sums[((k - 1) * TT + i) * frags * 64 + f * 64 + lane];
-                // D: lane (r, g) holds tokens 4 g .. 4 g + 3 of column r
-                if (16 * f + r < R) {
+        for (int i = 0; i < TT; ++i)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int t = 16 * i + 4 * g + q;
-                        if (t < count) p.low[((int64_t)part * p.T + tile.begin + t) * R + 16 * f + r] = acc[i][c][q];
-                    }
-                }
-            }
-        }
+            for (int q = 0; q < 4; ++q)
+                if (16 * i + 4 * g + q < count) o[(int64_t)(16 * i + 4 * g + q) * width] = acc[i][c][q];
+    }
 }
 
 // ---------------------------------------------------------------- up: y = add + scale B low
-// A wave takes 16 tokens of a tile and 64 outputs of one part at a time: four
-// fragments whose rows are dealt so that a lane ends up with 16 consecutive
-// outputs of one token.
+// A work-group takes a tile (TT fragments of 16 tokens) and a stretch of one part's
+// outputs.  low, with its scale and as bf16 terms, is made once in LDS; each of the
+// four waves then takes 64 outputs at a time: four fragments whose rows are dealt so
+// that a lane ends up with 16 consecutive outputs of one token.
 constexpr int WIDE = 64;
 
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void finish(const void *add, void *y, const float v[16], int n)
-{
-    if (VEC && n == 16) {
-        if (BF16) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const u32x4 a = ((const u32x4 *)add)[h];
-                u32x4 o;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[i] = to_bf16(__uint_as_float(a[i] << 16) + v[8 * h + 2 * i]) |
-                           to_bf16(__uint_as_float(a[i] & 0xffff0000u) + v[8 * h + 2 * i + 1]) << 16;
-                ((u32x4 *)y)[h] = o;
-            }
-        } else {
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-                ((f32x4 *)y)[h] = ((const f32x4 *)add)[h] + f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i < n) {
-            if (BF16) ((uint16_t *)y)[i] = (uint16_t)to_bf16(bf16_bits_to_f32(((const uint16_t *)add)[i]) + v[i]);
-            else ((float *)y)[i] = ((const float *)add)[i] + v[i];
-        }
-}
+template <bool BF16>
+struct Piece { u32x4 u[BF16 ? 2 : 4]; };         // 16 values
 
-template <bool BF16, bool VEC, int KS>           // KS: steps of 32 of the rank
+template <int TT, bool BF16, bool VEC, int KS>   // KS: steps of 32 of the rank
 __global__ __launch_bounds__(256) void adapter_up(AdapterPass p, int k_parts, int chunks)
 {
+    __shared__ bf16x8 low[3][TT][KS][64];
     const AdapterTile tile = p.tiles[blockIdx.x];
-    if (tile.adapter < -1) return;
-    const int size = blockDim.x / 4;             // tokens of a tile
-    const int end = tile.adapter < 0 ? p.T : p.offsets[tile.adapter + 1], left = min(size, end - tile.begin);
+    if (tile.adapter < -1 || (tile.adapter < 0 && p.add == p.y)) return;
+    const int end = tile.adapter < 0 ? p.T : p.offsets[tile.adapter + 1], count = min(16 * TT, end - tile.begin);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-    const int i0 = 16 * wave, count = min(16, left - i0);
-    if (count <= 0) return;
-    const int Np = p.N / p.parts, groups = (Np + WIDE - 1) / WIDE, R = p.parts * p.rank;
-    constexpr int ES = BF16 ? 2 : 4;
-    const int pos = tile.begin + i0 + min(r, count - 1), t = p.order[pos];
-    const char *const add = (const char *)p.add + (int64_t)t * p.ldadd * ES;
-    char *const y = (char *)p.y + (int64_t)t * p.ldy * ES;
-    const int per = (p.parts * groups + chunks - 1) / chunks, u0 = blockIdx.y * per, u1 = min(u0 + per, p.parts * groups);
-    if (tile.adapter < 0) {                      // tokens without an adapter: add as it is
-        if (p.add == p.y) return;
-        for (int u = u0; u < u1; ++u) {
-            const int q = u / groups, n0 = u % groups * WIDE + 16 * g;
-            if (r < count)
-                for (int i = 0; i < 16; ++i)
-                    if (n0 + i < Np) {
-                        const int64_t at = (int64_t)q * Np + n0 + i;
-                        if (BF16) ((uint16_t *)y)[at] = ((const uint16_t *)add)[at];
-                        else ((float *)y)[at] = ((const float *)add)[at];
-                    }
-        }
-        return;
-    }
-    const float factor = p.scale[tile.adapter] * (p.x_scale ? p.x_scale[t] : 1.0f);
-    bf16x8 low[KS][3];
-    int have = -1;
-    for (int u = u0; u < u1; ++u) {
-        const int q = u / groups, n0 = u % groups * WIDE;
-        // b's rows of this lane: output n0 + 16 (r / 4) + 4 f + r % 4 of fragment f; zero past the rank
-        u32x4 w[4][KS];
+    const int Np = p.N / p.parts, groups = (Np + WIDE - 1) / WIDE, r8 = (p.rank + 7) & ~7, width = p.parts * r8;
+    const int q = blockIdx.y / chunks, chunk = blockIdx.y % chunks, u1 = groups * (chunk + 1) / chunks;
+    constexpr int ES = BF16 ? 2 : 4, PW = BF16 ? 2 : 4;
+    int t[TT];
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            const int n = min(n0 + 16 * (r >> 2) + 4 * f + (r & 3), Np - 1);
-            const uint16_t *const row = p.b + ((int64_t)tile.adapter * p.N + (int64_t)q * Np + n) * p.ldb;
+    for (int i = 0; i < TT; ++i) t[i] = p.order[tile.begin + min(16 * i + r, count - 1)];
+    if (tile.adapter >= 0) {
+        const float scale = p.scale[tile.adapter];
 #pragma unroll
-            for (int s = 0; s < KS; ++s) w[f][s] = 32 * s + 8 * g < p.rank ? *(const u32x4 *)(row + 32 * s + 8 * g) : u32x4{0, 0, 0, 0};
-        }
-        if (q != have) {
-            have = q;
+        for (int i = 0; i < TT; ++i) {
+            if (i % 4 != wave) continue;
+            const int pos = tile.begin + min(16 * i + r, count - 1);
+            const float factor = scale * (p.x_scale ? p.x_scale[t[i]] : 1.0f);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                float v[8];
+                // the parts of K in order, eight parts' loads on their way together
+                constexpr int B = 8;
+                f32x4 v[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+                const int j = 32 * s + 8 * g;
+                if (j < p.rank)
+                    for (int k0 = 0; k0 < k_parts; k0 += B) {
+                        f32x4 x[B][2];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int j = 32 * s + 8 * g + i;
-                    v[i] = 0.0f;
-                    if (j < p.rank)
-                        for (int k = 0; k < k_parts; ++k) v[i] += p.low[((int64_t)k * p.T + pos) * R + q * p.rank + j];
-                    v[i] *= factor;
-                }
-                split(v, low[s]);
+                        for (int k = 0; k < B; ++k)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                x[k][h] = *(const f32x4 *)(p.low + ((int64_t)min(k0 + k, k_parts - 1) * p.T + pos) * width + q * r8 + j + 4 * h);
+#pragma unroll
+                        for (int k = 0; k < B; ++k)
+                            if (k0 + k < k_parts) {
+                                v[0] += x[k][0];
+                                v[1] += x[k][1];
+                            }
+                    }
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = j + e < p.rank ? v[e >> 2][e & 3] * factor : 0.0f;
+                bf16x8 terms[3];
+                split(f, terms);
+#pragma unroll
+                for (int m = 0; m < 3; ++m) low[m][i][s][lane] = terms[m];
             }
         }
-        float v[16];
+        __syncthreads();
+    }
+    for (int u = groups * chunk / chunks + wave; u < u1; u += 4) {
+        const int n0 = u * WIDE, outs = min(16, Np - n0 - 16 * g);     // of this lane (none if negative)
+        const int64_t at = (int64_t)q * Np + n0 + 16 * g;
+        u32x4 w[4][KS];
+        if (tile.adapter >= 0) {
+            // b's rows of this lane: output n0 + 16 (r / 4) + 4 f + r % 4 of fragment f; zero past the rank
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int f = 0; f < 4; ++f) {
+                const int n = min(n0 + 16 * (r >> 2) + 4 * f + (r & 3), Np - 1);
+                const uint16_t *const row = p.b + ((int64_t)tile.adapter * p.N + (int64_t)q * Np + n) * p.ldb;
 #pragma unroll
-            for (int m = 2; m >= 0; --m)
-#pragma unroll
-                for (int s = 0; s < KS; ++s) acc = mfma16x16x32(__builtin_bit_cast(bf16x8, w[f][s]), low[s][m], acc);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[4 * f + i] = acc[i];         // D: lane (r, g) holds rows 4 g + i of token r
+                for (int s = 0; s < KS; ++s) w[f][s] = 32 * s + 8 * g < p.rank ? *(const u32x4 *)(row + 32 * s + 8 * g) : u32x4{0, 0, 0, 0};
+            }
         }
-        const int64_t at = ((int64_t)q * Np + n0 + 16 * g) * ES;
-        if (r < count && n0 + 16 * g < Np) finish<BF16, VEC>(add + at, y + at, v, min(16, Np - n0 - 16 * g));
+        Piece<BF16> old[TT];
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+            if (VEC && outs == 16 && 16 * i + r < count) {
+#pragma unroll
+                for (int h = 0; h < PW; ++h) old[i].u[h] = ((const u32x4 *)((const char *)p.add + ((int64_t)t[i] * p.ldadd + at) * ES))[h];
+            }
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            if (16 * i >= count) break;
+            const bool whole = VEC && outs == 16 && 16 * i + r < count;
+            const int mine = 16 * i + r < count ? outs : 0;
+            const char *const add = (const char *)p.add + ((int64_t)t[i] * p.ldadd + at) * ES;
+            char *const y = (char *)p.y + ((int64_t)t[i] * p.ldy + at) * ES;
+            if (tile.adapter < 0) {              // no adapter: add as it is
+                if (whole) {
+#pragma unroll
+                    for (int h = 0; h < PW; ++h) ((u32x4 *)y)[h] = old[i].u[h];
+                } else
+                    for (int e = 0; e < mine; ++e) {
+                        if (BF16) ((uint16_t *)y)[e] = ((const uint16_t *)add)[e];
+                        else ((float *)y)[e] = ((const float *)add)[e];
+                    }
+                continue;
+            }
+            f32x4 acc[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int m = 2; m >= 0; --m)         // smallest term first
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const bf16x8 x = low[m][i][s][lane];
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) acc[f] = mfma16x16x32(__builtin_bit_cast(bf16x8, w[f][s]), x, acc[f]);
+                }
+            // D: lane (r, g) holds rows 4 g + i of token r: acc[f][i] is output 4 f + i of its 16
+            if (whole) {
+#pragma unroll
+                for (int h = 0; h < PW; ++h) {
+                    u32x4 o;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (BF16) {
+                            const int f = 2 * h + (e >> 1), j = 2 * (e & 1);
+                            o[e] = to_bf16(__uint_as_float(old[i].u[h][e] << 16) + acc[f][j]) |
+                                   to_bf16(__uint_as_float(old[i].u[h][e] & 0xffff0000u) + acc[f][j + 1]) << 16;
+                        } else o[e] = __float_as_uint(__uint_as_float(old[i].u[h][e]) + acc[h][e]);
+                    }
+                    ((u32x4 *)y)[h] = o;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (e < mine) {
+                        const float v = acc[e >> 2][e & 3];
+                        if (BF16) ((uint16_t *)y)[e] = (uint16_t)to_bf16(bf16_bits_to_f32(((const uint16_t *)add)[e]) + v);
+                        else ((float *)y)[e] = ((const float *)add)[e] + v;
+                    }
+            }
+        }
     }
 }
 
@@ -418,19 +457,20 @@ bool aligned(const void *p, int64_t ld, int size, int to) { return (uintptr_t)p 
 
 }  // namespace
 
-// Enough work-groups for the CUs: tiles of a large batch fill them, a few tokens are cut along K, into parts of at least 8 steps.
+// Enough work-groups for the CUs: tiles of a large batch fill them, a few tokens are cut along K, into parts of at least 8
+// steps (one a wave).
 int adapter_k_parts(int T, int K, int n)
 {
     const int tiles = std::min(T, (T + adapter_tile(T) - 1) / adapter_tile(T) + n), steps = (K + 31) / 32;
-    return std::max(1, std::min(512 / tiles, steps / 8));
+    return std::max(1, std::min(((adapter_tile(T) == 16 ? 512 : 256) + tiles - 1) / tiles, steps / 8));
 }
 
 size_t adapter_low_bytes(int T, int K, int width, int n)
 {
     int64_t rows = 0;
     for (int t = 1; t <= std::min(T, 512); ++t) rows = std::max(rows, (int64_t)t * adapter_k_parts(t, K, n));
-    // past 512 tokens a tile is 64: t * (512 / (t / 64)) rows at most, and t for one part
-    if (T > 512) rows = std::max(rows, std::min(std::max((int64_t)T, (int64_t)512 * 64), (int64_t)T * std::max(1, (K + 31) / 32 / 8)));
+    // past 512 tokens a tile is 64: t * (256 / (t / 64) + 1) rows at most
+    if (T > 512) rows = std::max(rows, std::min((int64_t)T + 256 * 64, (int64_t)T * std::max(1, (K + 31) / 32 / 8)));
     return (size_t)rows * width * sizeof(float);
 }
 
@@ -446,24 +486,40 @@ hipError_t launch_adapter_plan(const int32_t *ids, int T, int n, int32_t *order,
 
 hipError_t launch_adapter_down(const AdapterPass &p, hipStream_t s)
 {
-    const int parts = adapter_k_parts(p.T, p.K, p.n), frags = (p.parts * p.rank + 15) / 16, cw = frags >= 4 ? 4 : frags >= 2 ? 2 : 1;
-    const int tt = adapter_tile(p.T) / 16, es = p.kind == ADAPT_F32 ? 4 : p.kind == ADAPT_BF16 ? 2 : 1;
+    const int parts = adapter_k_parts(p.T, p.K, p.n), frags = (p.parts * p.rank + 15) / 16, tt = adapter_tile(p.T) / 16;
+    // as many column fragments to a wave as its registers hold: x is then read by one wave
+    const int most = tt == 4 && p.kind == ADAPT_F32 ? 4 : 8, cw = frags <= most ? 1 : frags <= 2 * most ? 2 : 4, ct = (frags + cw - 1) / cw;
+    const int es = p.kind == ADAPT_F32 ? 4 : p.kind == ADAPT_BF16 ? 2 : 1;
     const bool vec = aligned(p.x, p.ldx, es, std::min(16, 8 * es));
     const dim3 grid((unsigned)adapter_tiles(p.T, p.n), (unsigned)parts);
-    const size_t lds = (size_t)(4 / cw - 1) * tt * frags * 64 * 16;
-#define MOE_DOWN2(t, kind)                                                                        \
+    const size_t lds = (size_t)(NW / cw / 2) * tt * frags * 64 * 16;
+#define MOE_DOWN3(t, c, kind, v)                                                                  \
     do {                                                                                          \
-        if (vec) adapter_down<t, kind, true><<<grid, 256, lds, s>>>(p, parts, cw);                \
-        else adapter_down<t, kind, false><<<grid, 256, lds, s>>>(p, parts, cw);                   \
+        static DevSlots slots{};                                                                  \
+        const hipError_t e = lds_limit((const void *)adapter_down<t, c, kind, v>, slots, lds);    \
+        if (e != hipSuccess) return e;                                                            \
+        adapter_down<t, c, kind, v><<<grid, 64 * NW, lds, s>>>(p, parts, cw);                     \
     } while (0)
-#define MOE_DOWN(t)                                                                               \
+#define MOE_DOWN2(t, c, kind)                                                                     \
     do {                                                                                          \
-        if (p.kind == ADAPT_F32) MOE_DOWN2(t, ADAPT_F32);                                         \
-        else if (p.kind == ADAPT_BF16) MOE_DOWN2(t, ADAPT_BF16);                                  \
-        else MOE_DOWN2(t, ADAPT_I8);                                                              \
+        if (vec) MOE_DOWN3(t, c, kind, true);                                                     \
+        else MOE_DOWN3(t, c, kind, false);                                                        \
     } while (0)
-    if (tt == 1) MOE_DOWN(1);
-    else MOE_DOWN(4);
+#define MOE_DOWN1(t, kind, most)                                                                  \
+    do {                                                                                          \
+        if (ct <= 2) MOE_DOWN2(t, 2, kind);                                                       \
+        else MOE_DOWN2(t, most, kind);                                                            \
+    } while (0)
+#define MOE_DOWN(t, f32_most)                                                                     \
+    do {                                                                                          \
+        if (p.kind == ADAPT_F32) MOE_DOWN1(t, ADAPT_F32, f32_most);                               \
+        else if (p.kind == ADAPT_BF16) MOE_DOWN1(t, ADAPT_BF16, 8);                               \
+        else MOE_DOWN1(t, ADAPT_I8, 8);                                                           \
+    } while (0)
+    if (tt == 1) MOE_DOWN(1, 8);
+    else MOE_DOWN(4, 4);
+#undef MOE_DOWN1
+#undef MOE_DOWN3
 #undef MOE_DOWN
 #undef MOE_DOWN2
     return hipGetLastError();
@@ -471,24 +527,30 @@ hipError_t launch_adapter_down(const AdapterPass &p, hipStream_t s)
 
 hipError_t launch_adapter_up(const AdapterPass &p, hipStream_t s)
 {
-    const int parts = adapter_k_parts(p.T, p.K, p.n), tile = adapter_tile(p.T), es = p.y_bf16 ? 2 : 4;
-    const int tiles = adapter_tiles(p.T, p.n), units = p.parts * ((p.N / p.parts + WIDE - 1) / WIDE);
-    // about 8 waves a CU, each with a few units where the batch is large
-    const int waves = tiles * (tile / 16), chunks = std::max(1, std::min(units, 2048 / std::max(1, waves)));
+    const int parts = adapter_k_parts(p.T, p.K, p.n), es = p.y_bf16 ? 2 : 4;
+    const int tiles = adapter_tiles(p.T, p.n), groups = (p.N / p.parts + WIDE - 1) / WIDE;
+    // about 16 waves a CU, stretches of at least a group a wave
+    const int chunks = std::max(1, std::min((groups + 3) / 4, (1024 + tiles * p.parts - 1) / (tiles * p.parts)));
     const bool vec = aligned(p.y, p.ldy, es, 16) && aligned(p.add, p.ldadd, es, 16) && p.N / p.parts % (16 / es) == 0;
-    const dim3 grid((unsigned)tiles, (unsigned)chunks);
-#define MOE_UP2(bf, ks)                                                                           \
+    const dim3 grid((unsigned)tiles, (unsigned)(p.parts * chunks));
+#define MOE_UP3(t, bf, v)                                                                         \
     do {                                                                                          \
-        if (vec) adapter_up<bf, true, ks><<<grid, tile * 4, 0, s>>>(p, parts, chunks);            \
-        else adapter_up<bf, false, ks><<<grid, tile * 4, 0, s>>>(p, parts, chunks);               \
+        if (p.rank <= 32) adapter_up<t, bf, v, 1><<<grid, 256, 0, s>>>(p, parts, chunks);         \
+        else adapter_up<t, bf, v, 2><<<grid, 256, 0, s>>>(p, parts, chunks);                      \
     } while (0)
-#define MOE_UP(bf)                                                                                \
+#define MOE_UP2(t, bf)                                                                            \
     do {                                                                                          \
-        if (p.rank <= 32) MOE_UP2(bf, 1);                                                         \
-        else MOE_UP2(bf, 2);                                                                      \
+        if (vec) MOE_UP3(t, bf, true);                                                            \
+        else MOE_UP3(t, bf, false);                                                               \
     } while (0)
-    if (p.y_bf16) MOE_UP(true);
-    else MOE_UP(false);
+#define MOE_UP(t)                                                                                 \
+    do {                                                                                          \
+        if (p.y_bf16) MOE_UP2(t, true);                                                           \
+        else MOE_UP2(t, false);                                                                   \
+    } while (0)
+    if (adapter_tile(p.T) == 16) MOE_UP(1);
+    else MOE_UP(4);
+#undef MOE_UP3
 #undef MOE_UP
 #undef MOE_UP2
     return hipGetLastError();

@@ -341,7 +341,7 @@ int moe_adapter_plan(const int32_t *ids, int T, int n_adapters, int32_t *order, 
 size_t moe_adapters_workspace_bytes(const moe_adapter_set *W, int T)
 {
     if (T < 0 || T > ADAPT_MAX_T || check_adapters(W)) return 0;
-    return align_up(adapter_low_bytes(T, W->in_features, W->parts * W->rank, W->n_adapters));
+    return align_up(adapter_low_bytes(T, W->in_features, W->parts * ((W->rank + 7) & ~7), W->n_adapters));
 }
 
 int moe_adapters(const moe_adapter_set *W, int T, const int32_t *order, const int32_t *offsets, const int32_t *tiles,
@@ -363,7 +363,7 @@ int moe_adapters(const moe_adapter_set *W, int T, const int32_t *order, const in
         return set_error(MOE_ERR_INVALID_ARG, "x_scale comes with codes, and only with them, 4-byte aligned");
     if ((rc = check_rows("y", y, ldy, T, W->out_features, act_size(act_y)))) return rc;
     if ((rc = check_rows("add", add, ldadd, T, W->out_features, act_size(act_y)))) return rc;
-    const size_t need = (size_t)adapter_k_parts(T, W->in_features, W->n_adapters) * T * W->parts * W->rank * sizeof(float);
+    const size_t need = (size_t)adapter_k_parts(T, W->in_features, W->n_adapters) * T * W->parts * ((W->rank + 7) & ~7) * sizeof(float);
     if (!ws || (uintptr_t)ws % 16) return set_error(MOE_ERR_INVALID_ARG, "the workspace is NULL or not 16-byte aligned");
     if (ws_bytes < need) return set_error(MOE_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
     AdapterPass p{};
