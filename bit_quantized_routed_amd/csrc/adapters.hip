@@ -209,23 +209,28 @@ __device__ __forceinline__ void as_terms(const Raw &v, bf16x8 t[3])
 }
 
 // ---------------------------------------------------------------- down: low = x A^T
-// A work-group takes a tile (TT fragments of 16 tokens) and one part of K.  Its eight
-// waves share out the columns of low (cw ways, up to CT fragments each) and what is
-// left of the split the steps of 32 of K; these sums meet in LDS in a fixed order.
-constexpr int NW = 8;
+// A work-group takes a tile (TT fragments of 16 tokens) and one part of K.  Its waves
+// share out the columns of low (cw ways, up to CT fragments each) and what is left of
+// the split the part's K, in stretches of whole steps of 64 (a line of 128 bytes of
+// bf16, requested at once; neighbouring waves are on different L2 channels); these
+// sums meet in LDS in a fixed order.
+template <int TT>
+constexpr int down_waves() { return TT == 1 ? 8 : 4; }
+constexpr int DSTEP = 64;
 
 template <int TT, int CT, int KIND, bool VEC>
-__global__ __launch_bounds__(64 * NW) void adapter_down(AdapterPass p, int k_parts, int cw)
+__global__ __launch_bounds__(64 * down_waves<TT>()) void adapter_down(AdapterPass p, int k_parts, int cw)
 {
-    constexpr int NS = terms<KIND>();
+    constexpr int NS = terms<KIND>(), NW = down_waves<TT>();
     const AdapterTile tile = p.tiles[blockIdx.x];
     if (tile.adapter < 0) return;
     const int end = p.offsets[tile.adapter + 1], count = min(16 * TT, end - tile.begin);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const int R = p.parts * p.rank, frags = (R + 15) / 16, kw = NW / cw, wc = wave % cw, wk = wave / cw;
     const int r8 = (p.rank + 7) & ~7, width = p.parts * r8;
-    const int steps = (p.K + 31) / 32, part = blockIdx.y;
-    const int s0 = (int)((int64_t)steps * part / k_parts), s1 = (int)((int64_t)steps * (part + 1) / k_parts);
+    // this wave's steps: stretch part * kw + wk of k_parts * kw
+    const int steps = (p.K + DSTEP - 1) / DSTEP, part = blockIdx.y, stretch = part * kw + wk;
+    const int s0 = (int)((int64_t)steps * stretch / (k_parts * kw)), s1 = (int)((int64_t)steps * (stretch + 1) / (k_parts * kw));
     const void *row[TT];
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
@@ -245,34 +250,46 @@ __global__ __launch_bounds__(64 * NW) void adapter_down(AdapterPass p, int k_par
     for (int i = 0; i < TT; ++i)
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[i][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    Raw x[TT];
-    u32x4 w[CT];
-    // rows of A are zero past K, where there is anything
+    Raw x[2][TT];
+    u32x4 w[2][CT];
+    // the halves of a step are interleaved so that both of its loads touch whole lines; rows of A are zero past K, where there is anything
     auto load = [&](int s) {
         if (s >= s1) return;
 #pragma unroll
-        for (int i = 0; i < TT; ++i) x[i] = load_x<KIND, VEC>(row[i], 32 * s + 8 * g, p.K);
+        for (int h = 0; h < 2; ++h) {
+            const int k = DSTEP * s + 16 * g + 8 * h;
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
-            if (c < n_cols) w[c] = 32 * s + 8 * g < p.K ? *(const u32x4 *)(col[c] + 32 * s + 8 * g) : u32x4{0, 0, 0, 0};
+            for (int i = 0; i < TT; ++i) x[h][i] = load_x<KIND, VEC>(row[i], k, p.K);
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+                if (c < n_cols) w[h][c] = k < p.K ? *(const u32x4 *)(col[c] + k) : u32x4{0, 0, 0, 0};
+        }
     };
-    load(s0 + wk);
-    for (int s = s0 + wk; s < s1; s += kw) {
-        bf16x8 a[TT][3];
-        u32x4 b[CT];
+    load(s0);
+    for (int s = s0; s < s1; ++s) {
+        Raw xn[2][TT];
+        u32x4 b[2][CT];
 #pragma unroll
-        for (int i = 0; i < TT; ++i) as_terms<KIND>(x[i], a[i]);
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int c = 0; c < CT; ++c) b[c] = w[c];
-        load(s + kw);
+            for (int i = 0; i < TT; ++i) xn[h][i] = x[h][i];
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
-            if (c < n_cols) {
+            for (int c = 0; c < CT; ++c) b[h][c] = w[h][c];
+        }
+        load(s + 1);
 #pragma unroll
-                for (int i = 0; i < TT; ++i)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int q = NS - 1; q >= 0; --q)                  // smallest term first
-                        acc[i][c] = mfma16x16x32(a[i][q], __builtin_bit_cast(bf16x8, b[c]), acc[i][c]);
+            for (int i = 0; i < TT; ++i) {
+                bf16x8 a[3];
+                as_terms<KIND>(xn[h][i], a);
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+                    if (c < n_cols) {
+#pragma unroll
+                        for (int q = NS - 1; q >= 0; --q)              // smallest term first
+                            acc[i][c] = mfma16x16x32(a[q], __builtin_bit_cast(bf16x8, b[h][c]), acc[i][c]);
+                    }
             }
     }
     // sums over the waves that share these columns, by halves
@@ -457,20 +474,20 @@ bool aligned(const void *p, int64_t ld, int size, int to) { return (uintptr_t)p 
 
 }  // namespace
 
-// Enough work-groups for the CUs: tiles of a large batch fill them, a few tokens are cut along K, into parts of at least 8
-// steps (one a wave).
+// Work-groups of up to two a CU at once: tiles of a large batch fill them, a few tokens are cut along K, into parts of at least
+// 256.
 int adapter_k_parts(int T, int K, int n)
 {
     const int tiles = std::min(T, (T + adapter_tile(T) - 1) / adapter_tile(T) + n), steps = (K + 31) / 32;
-    return std::max(1, std::min(((adapter_tile(T) == 16 ? 512 : 256) + tiles - 1) / tiles, steps / 8));
+    return std::max(1, std::min(512 / tiles, steps / 8));
 }
 
 size_t adapter_low_bytes(int T, int K, int width, int n)
 {
     int64_t rows = 0;
     for (int t = 1; t <= std::min(T, 512); ++t) rows = std::max(rows, (int64_t)t * adapter_k_parts(t, K, n));
-    // past 512 tokens a tile is 64: t * (256 / (t / 64) + 1) rows at most
-    if (T > 512) rows = std::max(rows, std::min((int64_t)T + 256 * 64, (int64_t)T * std::max(1, (K + 31) / 32 / 8)));
+    // past 512 tokens a tile is 64: t * (512 / (t / 64)) rows at most, and t of one part
+    if (T > 512) rows = std::max(rows, std::min(std::max((int64_t)T, (int64_t)512 * 64), (int64_t)T * std::max(1, (K + 31) / 32 / 8)));
     return (size_t)rows * width * sizeof(float);
 }
 
@@ -487,37 +504,37 @@ hipError_t launch_adapter_plan(const int32_t *ids, int T, int n, int32_t *order,
 hipError_t launch_adapter_down(const AdapterPass &p, hipStream_t s)
 {
     const int parts = adapter_k_parts(p.T, p.K, p.n), frags = (p.parts * p.rank + 15) / 16, tt = adapter_tile(p.T) / 16;
-    // as many column fragments to a wave as its registers hold: x is then read by one wave
-    const int most = tt == 4 && p.kind == ADAPT_F32 ? 4 : 8, cw = frags <= most ? 1 : frags <= 2 * most ? 2 : 4, ct = (frags + cw - 1) / cw;
+    // up to four column fragments a wave; the other waves divide K
+    const int cw = frags <= 4 ? 1 : frags <= 8 ? 2 : 4, ct = (frags + cw - 1) / cw, waves = tt == 1 ? down_waves<1>() : down_waves<4>();
     const int es = p.kind == ADAPT_F32 ? 4 : p.kind == ADAPT_BF16 ? 2 : 1;
     const bool vec = aligned(p.x, p.ldx, es, std::min(16, 8 * es));
     const dim3 grid((unsigned)adapter_tiles(p.T, p.n), (unsigned)parts);
-    const size_t lds = (size_t)(NW / cw / 2) * tt * frags * 64 * 16;
+    const size_t lds = (size_t)(waves / cw / 2) * tt * frags * 64 * 16;
 #define MOE_DOWN3(t, c, kind, v)                                                                  \
     do {                                                                                          \
         static DevSlots slots{};                                                                  \
         const hipError_t e = lds_limit((const void *)adapter_down<t, c, kind, v>, slots, lds);    \
         if (e != hipSuccess) return e;                                                            \
-        adapter_down<t, c, kind, v><<<grid, 64 * NW, lds, s>>>(p, parts, cw);                     \
+        adapter_down<t, c, kind, v><<<grid, 64 * waves, lds, s>>>(p, parts, cw);                  \
     } while (0)
 #define MOE_DOWN2(t, c, kind)                                                                     \
     do {                                                                                          \
         if (vec) MOE_DOWN3(t, c, kind, true);                                                     \
         else MOE_DOWN3(t, c, kind, false);                                                        \
     } while (0)
-#define MOE_DOWN1(t, kind, most)                                                                  \
+#define MOE_DOWN1(t, kind)                                                                        \
     do {                                                                                          \
         if (ct <= 2) MOE_DOWN2(t, 2, kind);                                                       \
-        else MOE_DOWN2(t, most, kind);                                                            \
+        else MOE_DOWN2(t, 4, kind);                                                               \
     } while (0)
-#define MOE_DOWN(t, f32_most)                                                                     \
+#define MOE_DOWN(t)                                                                               \
     do {                                                                                          \
-        if (p.kind == ADAPT_F32) MOE_DOWN1(t, ADAPT_F32, f32_most);                               \
-        else if (p.kind == ADAPT_BF16) MOE_DOWN1(t, ADAPT_BF16, 8);                               \
-        else MOE_DOWN1(t, ADAPT_I8, 8);                                                           \
+        if (p.kind == ADAPT_F32) MOE_DOWN1(t, ADAPT_F32);                                         \
+        else if (p.kind == ADAPT_BF16) MOE_DOWN1(t, ADAPT_BF16);                                  \
+        else MOE_DOWN1(t, ADAPT_I8);                                                              \
     } while (0)
-    if (tt == 1) MOE_DOWN(1, 8);
-    else MOE_DOWN(4, 4);
+    if (tt == 1) MOE_DOWN(1);
+    else MOE_DOWN(4);
 #undef MOE_DOWN1
 #undef MOE_DOWN3
 #undef MOE_DOWN
