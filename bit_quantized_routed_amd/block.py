@@ -7,6 +7,10 @@ quantized routed experts, and the shared expert in 8 bits.
     y  += W_down silu(W_gate n) * (W_up n)    int8 rows and weights
 
 x of the next block is y: it joins the residual in that block's norm.
+
+`MoeBlock.__call__` runs the operators one after the other, for any number of tokens and with the low-rank adapters of
+the tokens' requests on the shared expert's projections; `MoeBlock.decode` runs the block of up to 16 tokens in two
+kernels, with the shared expert's activations in full (they are not cut to 8 bits).
 """
 from __future__ import annotations
 
@@ -14,6 +18,18 @@ import bit_quantized_routed_amd as M
 
 # tokens up to which the decode path of the routed experts is the faster one
 DECODE_TOKENS = 64
+# tokens that moe_block_decode takes
+FEW_TOKENS = 16
+
+
+class StepAdapters:
+    """The adapters of one step at one block: the step's plan (M.AdapterPlan, filled by M.adapter_plan) and the weights beside
+    the shared expert's gate/up rows (two parts) and its down rows, either of them None."""
+
+    def __init__(self, plan, gate_up=None, down=None, device="cuda"):
+        self.plan, self.gate_up, self.down = plan, gate_up, down
+        sizes = [w.workspace(plan.T, device) for w in (gate_up, down) if w is not None]
+        self.ws = max(sizes, key=lambda t: t.nbytes) if sizes else None
 
 
 class BlockBuffers:
@@ -34,6 +50,7 @@ class BlockBuffers:
         self.ws_route = block.router.workspace(T, device)
         self.ws_ffn = block.layer.workspace(T, self.path, device)
         self.ws_up, self.ws_down = block.gate_up.workspace(T, device), block.down.workspace(T, device)
+        self.ws_few = block.few.workspace(T, device) if block.few is not None and T <= FEW_TOKENS else None
 
 
 class MoeBlock:
@@ -50,14 +67,33 @@ class MoeBlock:
                              % (gate_up.out_features, gate_up.in_features, down.out_features, down.in_features, self.hidden))
         if (router.hidden, router.n_experts, router.top_k) != (layer.hidden, layer.n_experts, layer.top_k):
             raise ValueError("router and layer differ in hidden, experts or top k")
+        self.few = M.BlockWeights(norm, router, layer, gate_up, down) if self._takes_few(layer.c) else None
 
-    def __call__(self, x, residual, b: BlockBuffers, stream=None):
+    def _takes_few(self, c):
+        """Whether moe_block_decode takes these weights."""
+        return ((c.fmt_gate_up, c.fmt_down) == (M.FMT_CB2, M.FMT_Q2K) and not c.flags and not c.expert_slot
+                and max(c.hidden, c.inter, self.sh_inter) <= 8192 and c.n_experts <= 512 and c.top_k <= 16)
+
+    def decode(self, x, residual, b: BlockBuffers, stream=None):
+        """The block for up to 16 tokens in two kernels (see moe_block_decode).  x, residual: [T, H] rows; residual is updated in
+        place.  Returns b.y.  Buffers that may be in use at the same time need a BlockBuffers each."""
+        if b.ws_few is None:
+            raise ValueError("decode takes up to %d tokens of a CB2 / Q2_K layer, of at most 8192 features, 512 experts and top 16"
+                             % FEW_TOKENS)
+        M.block_decode(self.few, x, residual, residual, b.y, b.routing, b.ws_few, stream)
+        return b.y
+
+    def __call__(self, x, residual, b: BlockBuffers, stream=None, adapters: StepAdapters | None = None):
         """x, residual: [T, H] rows; residual is updated in place.  Returns b.y."""
         M.residual_norm(self.norm, x, residual, residual, b.n, b.q, b.q_scale, stream)
         M.route_scored(self.router, b.n, b.routing, b.ws_route, stream)
         ffn = M.ffn_decode if b.path == M.PATH_DECODE else M.ffn_prefill
         ffn(self.layer, b.n, M.ACT_BF16, b.T, b.routing, b.y, b.ws_ffn, stream)
         M.linear_i8(self.gate_up, b.q, b.q_scale, b.gate_up, None, b.ws_up, stream)
+        if adapters is not None and adapters.gate_up is not None:
+            M.adapters(adapters.gate_up, adapters.plan, b.n, None, b.gate_up, None, adapters.ws, stream)
         M.quant_i8(b.gate_up, b.h, b.h_scale, True, stream)
         M.linear_i8(self.down, b.h, b.h_scale, b.y, b.y, b.ws_down, stream)
+        if adapters is not None and adapters.down is not None:
+            M.adapters(adapters.down, adapters.plan, b.h, b.h_scale, b.y, None, adapters.ws, stream)
         return b.y

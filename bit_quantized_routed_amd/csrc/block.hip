@@ -840,6 +840,7 @@ __device__ __forceinline__ bool down_items(const BlockPass &p, int item, int bas
         __syncthreads();
         item = (int)next - base;
         __syncthreads();                         // and the sums are read
+        if (item < 0) return false;
     }
     return true;
 }
@@ -867,17 +868,24 @@ __device__ __noinline__ void give_up(Args pa)
 __device__ __noinline__ void load_list(Args pa, int n_list)
 {
     const BlockPass &p = args_of(pa);
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, n = p.T * p.k;
     Small &l = small();
+    // in bounds whatever another call may have left there
+    int e = 0, first = 0, count = 0;
     if (tid < n_list) {
         const int entry = peek(p.list + tid);
-        l.entry[tid] = entry;
-        for (int i = 0; i < entry >> 20; ++i) l.seg[(entry >> 10 & 1023) + i] = (int16_t)tid;
+        e = min(entry & 1023, p.E - 1);
+        first = min(entry >> 10 & 1023, n - 1);
+        count = min(entry >> 20 & 31, n - first);
+        l.entry[tid] = e | first << 10 | count << 20;
     }
-    if (tid < p.T * p.k) {
-        l.tok[tid] = (int16_t)peek(p.list + 256 + tid);
+    if (tid < n) {
+        l.tok[tid] = (int16_t)min(max(peek(p.list + 256 + tid), 0), p.T - 1);
         l.weight[tid] = peek((const float *)p.list + 512 + tid);
+        l.seg[tid] = 0;
     }
+    __syncthreads();
+    for (int i = 0; i < count; ++i) l.seg[first + i] = (int16_t)tid;
     __syncthreads();
 }
 
@@ -924,20 +932,20 @@ __global__ __launch_bounds__(NT) void block_kernel(BlockPass p)
     if (!resident && p.T <= p.slots) stage_tokens(pa, 0, nullptr, p.T);
     if (tid == 0) word = wait_for(ctl + C_LIST, 1) ? peek(ctl + C_LIST) : 0;
     __syncthreads();
-    const int n_list = (int)word, n_routed = n_list * p.nf;
-    if (n_list == 0) {
+    const int n_list = min((int)word, p.T * p.k), n_routed = n_list * p.nf;
+    if (n_list <= 0) {
         give_up(pa);
         return;
     }
     load_list(pa, n_list);
-    while (item < n_routed) {
+    while (item >= 0 && item < n_routed) {       // a negative one: the counters are another call's
         routed_item(p, pa, item);
         arrive(ctl, C_ROUTED, next);
         __syncthreads();
         item = (int)next - 1 - p.t_shared;
         __syncthreads();
     }
-    if (!down_items(p, item - n_routed, 1 + p.t_shared + n_routed, n_list, next, word)) give_up(pa);
+    if (item < 0 || !down_items(p, item - n_routed, 1 + p.t_shared + n_routed, n_list, next, word)) give_up(pa);
 }
 
 }  // namespace

@@ -356,6 +356,9 @@ int moe_adapters(const moe_adapter_set *W, int T, const int32_t *order, const in
     if (prof) prof->n_launches = 0;
     if (T == 0) return MOE_OK;
     if (T > ADAPT_MAX_T) return set_error(MOE_ERR_UNSUPPORTED, "T=%d: more tokens than one plan takes", T);
+    const size_t need = (size_t)adapter_k_parts(T, W->in_features, W->n_adapters) * T * W->parts * ((W->rank + 7) & ~7) * sizeof(float);
+    if (!ws || (uintptr_t)ws % 16) return set_error(MOE_ERR_INVALID_ARG, "the workspace is NULL or not 16-byte aligned");
+    if (ws_bytes < need) return set_error(MOE_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
     if (!order || !offsets || !tiles) return set_error(MOE_ERR_INVALID_ARG, "the plan is NULL");
     if (((uintptr_t)order | (uintptr_t)offsets) % 4 || (uintptr_t)tiles % 8) return set_error(MOE_ERR_INVALID_ARG, "the plan is not aligned");
     if ((rc = check_rows("x", x, ldx, T, W->in_features, kind_x == MOE_ADAPT_F32 ? 4 : kind_x == MOE_ADAPT_BF16 ? 2 : 1))) return rc;
@@ -363,9 +366,6 @@ int moe_adapters(const moe_adapter_set *W, int T, const int32_t *order, const in
         return set_error(MOE_ERR_INVALID_ARG, "x_scale comes with codes, and only with them, 4-byte aligned");
     if ((rc = check_rows("y", y, ldy, T, W->out_features, act_size(act_y)))) return rc;
     if ((rc = check_rows("add", add, ldadd, T, W->out_features, act_size(act_y)))) return rc;
-    const size_t need = (size_t)adapter_k_parts(T, W->in_features, W->n_adapters) * T * W->parts * ((W->rank + 7) & ~7) * sizeof(float);
-    if (!ws || (uintptr_t)ws % 16) return set_error(MOE_ERR_INVALID_ARG, "the workspace is NULL or not 16-byte aligned");
-    if (ws_bytes < need) return set_error(MOE_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
     AdapterPass p{};
     p.T = T; p.K = W->in_features; p.N = W->out_features; p.n = W->n_adapters; p.rank = W->rank; p.parts = W->parts;
     p.kind = kind_x == MOE_ADAPT_F32 ? ADAPT_F32 : kind_x == MOE_ADAPT_BF16 ? ADAPT_BF16 : ADAPT_I8;
