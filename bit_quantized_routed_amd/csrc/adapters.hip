@@ -43,15 +43,35 @@ __global__ __launch_bounds__(PLAN_NT) void adapter_plan(const int32_t *ids, int 
     for (int i = tid; i < PLAN_NW * bins; i += PLAN_NT) count[i] = 0;
     const int stretch = ((T + PLAN_NW - 1) / PLAN_NW + 63) / 64 * 64, begin = min(T, wave * stretch), end = min(T, begin + stretch);
     auto bin = [&](int id) { return id >= 0 && id < n ? id : n; };
+    // walks the wave's stretch in order: step(token, bin, lanes of the same bin), bin -1 past the end
+    const int bits = 32 - __clz(n);
+    auto walk = [&](auto step) {
+        for (int t0 = begin; t0 < end; t0 += 64 * BATCH) {
+            int id[BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) id[i] = t0 + 64 * i + lane < end ? bin(ids[t0 + 64 * i + lane]) : -1;
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                if (t0 + 64 * i >= end) break;
+                uint64_t same = __ballot(id[i] >= 0);
+                for (int q = 0; q < bits; ++q) {
+                    const uint64_t set = __ballot(id[i] >> q & 1);
+                    same &= id[i] >> q & 1 ? set : ~set;
+                }
+                // the wave's LDS operations run in order
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_wave_barrier();
+                if (id[i] >= 0) step(t0 + 64 * i + lane, id[i], same);
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
+    };
     __syncthreads();
-    for (int t0 = begin + lane; t0 < end; t0 += 64 * BATCH) {
-        int id[BATCH];
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) id[i] = t0 + 64 * i < end ? ids[t0 + 64 * i] : 0;
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i)
-            if (t0 + 64 * i < end) atomicAdd(&mine[bin(id[i])], 1);
-    }
+    // one lane counts for all of a bin (64 lanes' atomics on one word took 11 us of 8192 tokens in runs)
+    walk([&](int, int b, uint64_t same) {
+        if (same >> lane >> 1 == 0) mine[b] += __popcll(same);
+    });
     __syncthreads();
     // thread b: bin b (bins <= 1025: thread 0 has the last one too); first the sums over the waves
     int carry[2] = {0, 0};
@@ -107,31 +127,13 @@ __global__ __launch_bounds__(PLAN_NT) void adapter_plan(const int32_t *ids, int 
         tiles[i] = x;
     }
     __syncthreads();
-    const int bits = 32 - __clz(n);
-    for (int t0 = begin; t0 < end; t0 += 64 * BATCH) {
-        int id[BATCH];
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) id[i] = t0 + 64 * i + lane < end ? bin(ids[t0 + 64 * i + lane]) : -1;
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            if (t0 + 64 * i >= end) break;
-            uint64_t same = __ballot(id[i] >= 0);
-            for (int q = 0; q < bits; ++q) {
-                const uint64_t set = __ballot(id[i] >> q & 1);
-                same &= id[i] >> q & 1 ? set : ~set;
-            }
-            if (id[i] >= 0) {
-                const int rank = __popcll(same & ((1ull << lane) - 1ull)), at = mine[id[i]] + rank;
-                order[at] = t0 + 64 * i + lane;
-                // the group's last lane moves the position on; the wave's LDS operations run in order
-                asm volatile("" ::: "memory");
-                __builtin_amdgcn_wave_barrier();
-                if (same >> lane >> 1 == 0) mine[id[i]] = at + 1;
-            }
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_wave_barrier();
-        }
-    }
+    walk([&](int t, int b, uint64_t same) {
+        const int at = mine[b] + __popcll(same & ((1ull << lane) - 1ull));
+        order[at] = t;
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
+        if (same >> lane >> 1 == 0) mine[b] = at + 1;                  // the last lane moves the position on
+    });
 }
 
 // ---------------------------------------------------------------- values as bf16 terms
@@ -140,12 +142,15 @@ constexpr int terms() { return KIND == ADAPT_F32 ? 3 : 1; }
 
 struct Raw { u32x4 u[2]; };                      // eight values as they are in memory
 
-// eight values of a row from k on, zeros past K
+// Eight values of a row from k on.  VEC: aligned rows of K % 8 == 0 values, and past K the row's last eight, without a
+// branch (A is zero there, and what an infinity times that zero is comes to its own token alone); else element by element,
+// zeros past K.
 template <int KIND, bool VEC>
 __device__ __forceinline__ Raw load_x(const void *row, int k, int K)
 {
     Raw v;
-    if (VEC && k + 8 <= K) {
+    if (VEC) {
+        k = min(k, K - 8);
         if (KIND == ADAPT_F32) {
             v.u[0] = *(const u32x4 *)((const float *)row + k);
             v.u[1] = *(const u32x4 *)((const float *)row + k + 4);
@@ -238,11 +243,10 @@ __global__ __launch_bounds__(64 * down_waves<TT>()) void adapter_down(AdapterPas
         row[i] = (const char *)p.x + (int64_t)t * p.ldx * (KIND == ADAPT_F32 ? 4 : KIND == ADAPT_BF16 ? 2 : 1);
     }
     const uint16_t *col[CT];
-    int n_cols = 0;
+    // fragments past the last one compute it again and are not stored
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
         const int f = wc + c * cw;
-        if (f < frags) n_cols = c + 1;
         col[c] = p.a + ((int64_t)tile.adapter * R + min(16 * f + r, R - 1)) * p.lda;
     }
     f32x4 acc[TT][CT];
@@ -250,47 +254,51 @@ __global__ __launch_bounds__(64 * down_waves<TT>()) void adapter_down(AdapterPas
     for (int i = 0; i < TT; ++i)
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[i][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    Raw x[2][TT];
-    u32x4 w[2][CT];
-    // the halves of a step are interleaved so that both of its loads touch whole lines; rows of A are zero past K, where there is anything
-    auto load = [&](int s) {
-        if (s >= s1) return;
+    struct Step { Raw x[2][TT]; u32x4 w[2][CT]; };
+    const int last = ((p.K + 7) & ~7) - 8;       // rows of A have zeros up to a multiple of 8
+    auto load = [&](int s, Step &v) {
+        s = min(s, s1 - 1);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int k = DSTEP * s + 16 * g + 8 * h;
+            const int k = DSTEP * s + 32 * h + 8 * g;
 #pragma unroll
-            for (int i = 0; i < TT; ++i) x[h][i] = load_x<KIND, VEC>(row[i], k, p.K);
+            for (int i = 0; i < TT; ++i) v.x[h][i] = load_x<KIND, VEC>(row[i], k, p.K);
 #pragma unroll
-            for (int c = 0; c < CT; ++c)
-                if (c < n_cols) w[h][c] = k < p.K ? *(const u32x4 *)(col[c] + k) : u32x4{0, 0, 0, 0};
+            for (int c = 0; c < CT; ++c) v.w[h][c] = *(const u32x4 *)(col[c] + min(k, last));
         }
     };
-    load(s0);
-    for (int s = s0; s < s1; ++s) {
-        Raw xn[2][TT];
-        u32x4 b[2][CT];
+    auto multiply = [&](int s, Step &v) {
+        if (DSTEP * (s + 1) > last + 8) {        // the row's last step: nothing past its end
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < 2; ++h)
+                if (DSTEP * s + 32 * h + 8 * g > last) {
 #pragma unroll
-            for (int i = 0; i < TT; ++i) xn[h][i] = x[h][i];
-#pragma unroll
-            for (int c = 0; c < CT; ++c) b[h][c] = w[h][c];
+                    for (int c = 0; c < CT; ++c) v.w[h][c] = u32x4{0, 0, 0, 0};
+                }
         }
-        load(s + 1);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < TT; ++i) {
                 bf16x8 a[3];
-                as_terms<KIND>(xn[h][i], a);
+                as_terms<KIND>(v.x[h][i], a);
 #pragma unroll
                 for (int c = 0; c < CT; ++c)
-                    if (c < n_cols) {
 #pragma unroll
-                        for (int q = NS - 1; q >= 0; --q)              // smallest term first
-                            acc[i][c] = mfma16x16x32(a[q], __builtin_bit_cast(bf16x8, b[h][c]), acc[i][c]);
-                    }
+                    for (int q = NS - 1; q >= 0; --q)                  // smallest term first
+                        acc[i][c] = mfma16x16x32(a[q], __builtin_bit_cast(bf16x8, v.w[h][c]), acc[i][c]);
             }
+    };
+    // two steps by name: a copy of the one would wait for its loads
+    if (s0 < s1) {
+        Step even, odd;
+        load(s0, even);
+        for (int s = s0; s < s1; s += 2) {
+            load(s + 1, odd);
+            multiply(s, even);
+            load(s + 2, even);
+            if (s + 1 < s1) multiply(s + 1, odd);
+        }
     }
     // sums over the waves that share these columns, by halves
     extern __shared__ f32x4 sums[];              // [kw / 2][TT][column fragments][64]
@@ -299,7 +307,7 @@ __global__ __launch_bounds__(64 * down_waves<TT>()) void adapter_down(AdapterPas
         if (wk >= half && wk < 2 * half) {
 #pragma unroll
             for (int c = 0; c < CT; ++c)
-                if (c < n_cols) {
+                if (wc + c * cw < frags) {
 #pragma unroll
                     for (int i = 0; i < TT; ++i) at[(i * frags + c * cw) * 64] = acc[i][c];
                 }
@@ -308,7 +316,7 @@ __global__ __launch_bounds__(64 * down_waves<TT>()) void adapter_down(AdapterPas
         if (wk < half) {
 #pragma unroll
             for (int c = 0; c < CT; ++c)
-                if (c < n_cols) {
+                if (wc + c * cw < frags) {
 #pragma unroll
                     for (int i = 0; i < TT; ++i) acc[i][c] += at[(i * frags + c * cw) * 64];
                 }
@@ -319,7 +327,7 @@ __global__ __launch_bounds__(64 * down_waves<TT>()) void adapter_down(AdapterPas
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
         const int f = 16 * (wc + c * cw) + r;    // D: lane (r, g) holds tokens 4 g .. 4 g + 3 of column r
-        if (c >= n_cols || f >= R) continue;
+        if (f >= R) continue;
         float *const o = p.low + ((int64_t)part * p.T + tile.begin) * width + f / p.rank * r8 + f % p.rank;
 #pragma unroll
         for (int i = 0; i < TT; ++i)
@@ -333,7 +341,9 @@ __global__ __launch_bounds__(64 * down_waves<TT>()) void adapter_down(AdapterPas
 // A work-group takes a tile (TT fragments of 16 tokens) and a stretch of one part's
 // outputs.  low, with its scale and as bf16 terms, is made once in LDS; each of the
 // four waves then takes 64 outputs at a time: four fragments whose rows are dealt so
-// that a lane ends up with 16 consecutive outputs of one token.
+// that a lane's outputs are 16-byte pieces of one token and four lanes hold 64 bytes
+// in a row (with 16 outputs in a row a lane, every lane of a store was a segment of
+// its own: 512 x 7168 from rank 32 took 16 us).
 constexpr int WIDE = 64;
 
 template <bool BF16>
@@ -349,10 +359,35 @@ __global__ __launch_bounds__(256) void adapter_up(AdapterPass p, int k_parts, in
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const int Np = p.N / p.parts, groups = (Np + WIDE - 1) / WIDE, r8 = (p.rank + 7) & ~7, width = p.parts * r8;
     const int q = blockIdx.y / chunks, chunk = blockIdx.y % chunks, u1 = groups * (chunk + 1) / chunks;
-    constexpr int ES = BF16 ? 2 : 4, PW = BF16 ? 2 : 4;
+    // a lane's piece h: PV outputs from n0 + at(h) on
+    constexpr int ES = BF16 ? 2 : 4, PW = BF16 ? 2 : 4, PV = 16 / PW;
+    auto at = [&](int h) { return 4 * PV * h + PV * g; };
     int t[TT];
 #pragma unroll
     for (int i = 0; i < TT; ++i) t[i] = p.order[tile.begin + min(16 * i + r, count - 1)];
+    // what a group of 64 outputs reads: b's rows of this lane (the outputs of fragment f, zero past the rank) and add; the first group's are on their way while low is made
+    u32x4 w[4][KS];
+    Piece<BF16> old[TT];
+    auto load = [&](int u) {
+        const int n0 = min(u, groups - 1) * WIDE;
+        // no branches: what lies past the end is clamped, and not stored; past the rank low is zero
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            const int n = min(n0 + (BF16 ? 32 * (f >> 1) + 8 * (r >> 2) + 4 * (f & 1) + (r & 3) : 16 * f + r), Np - 1);
+            const uint16_t *const row = p.b + ((int64_t)max(tile.adapter, 0) * p.N + (int64_t)q * Np + n) * p.ldb;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) w[f][s] = *(const u32x4 *)(row + min(32 * s + 8 * g, r8 - 8));
+        }
+        if (VEC) {
+#pragma unroll
+            for (int i = 0; i < TT; ++i)
+#pragma unroll
+                for (int h = 0; h < PW; ++h)
+                    old[i].u[h] = *(const u32x4 *)((const char *)p.add + ((int64_t)t[i] * p.ldadd + (int64_t)q * Np + min(n0 + at(h), Np - PV)) * ES);
+        }
+    };
+    const int u0 = groups * chunk / chunks + wave;
+    load(u0);
     if (tile.adapter >= 0) {
         const float scale = p.scale[tile.adapter];
 #pragma unroll
@@ -392,81 +427,185 @@ __global__ __launch_bounds__(256) void adapter_up(AdapterPass p, int k_parts, in
         }
         __syncthreads();
     }
-    for (int u = groups * chunk / chunks + wave; u < u1; u += 4) {
-        const int n0 = u * WIDE, outs = min(16, Np - n0 - 16 * g);     // of this lane (none if negative)
-        const int64_t at = (int64_t)q * Np + n0 + 16 * g;
-        u32x4 w[4][KS];
-        if (tile.adapter >= 0) {
-            // b's rows of this lane: output n0 + 16 (r / 4) + 4 f + r % 4 of fragment f; zero past the rank
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                const int n = min(n0 + 16 * (r >> 2) + 4 * f + (r & 3), Np - 1);
-                const uint16_t *const row = p.b + ((int64_t)tile.adapter * p.N + (int64_t)q * Np + n) * p.ldb;
-#pragma unroll
-                for (int s = 0; s < KS; ++s) w[f][s] = 32 * s + 8 * g < p.rank ? *(const u32x4 *)(row + 32 * s + 8 * g) : u32x4{0, 0, 0, 0};
-            }
-        }
-        Piece<BF16> old[TT];
-#pragma unroll
-        for (int i = 0; i < TT; ++i)
-            if (VEC && outs == 16 && 16 * i + r < count) {
-#pragma unroll
-                for (int h = 0; h < PW; ++h) old[i].u[h] = ((const u32x4 *)((const char *)p.add + ((int64_t)t[i] * p.ldadd + at) * ES))[h];
-            }
+    for (int u = u0; u < u1; u += 4) {
+        if (u > u0) load(u);
+        const int n0 = u * WIDE;
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
-            if (16 * i >= count) break;
-            const bool whole = VEC && outs == 16 && 16 * i + r < count;
-            const int mine = 16 * i + r < count ? outs : 0;
-            const char *const add = (const char *)p.add + ((int64_t)t[i] * p.ldadd + at) * ES;
-            char *const y = (char *)p.y + ((int64_t)t[i] * p.ldy + at) * ES;
-            if (tile.adapter < 0) {              // no adapter: add as it is
-                if (whole) {
-#pragma unroll
-                    for (int h = 0; h < PW; ++h) ((u32x4 *)y)[h] = old[i].u[h];
-                } else
-                    for (int e = 0; e < mine; ++e) {
-                        if (BF16) ((uint16_t *)y)[e] = ((const uint16_t *)add)[e];
-                        else ((float *)y)[e] = ((const float *)add)[e];
-                    }
-                continue;
-            }
+            if (TT == 1 && 16 * i >= count) break;
             f32x4 acc[4];
 #pragma unroll
             for (int f = 0; f < 4; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (tile.adapter >= 0) {
 #pragma unroll
-            for (int m = 2; m >= 0; --m)         // smallest term first
+                for (int m = 2; m >= 0; --m)     // smallest term first
 #pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const bf16x8 x = low[m][i][s][lane];
+                    for (int s = 0; s < KS; ++s) {
+                        const bf16x8 x = low[m][i][s][lane];
 #pragma unroll
-                    for (int f = 0; f < 4; ++f) acc[f] = mfma16x16x32(__builtin_bit_cast(bf16x8, w[f][s]), x, acc[f]);
-                }
-            // D: lane (r, g) holds rows 4 g + i of token r: acc[f][i] is output 4 f + i of its 16
-            if (whole) {
-#pragma unroll
-                for (int h = 0; h < PW; ++h) {
-                    u32x4 o;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (BF16) {
-                            const int f = 2 * h + (e >> 1), j = 2 * (e & 1);
-                            o[e] = to_bf16(__uint_as_float(old[i].u[h][e] << 16) + acc[f][j]) |
-                                   to_bf16(__uint_as_float(old[i].u[h][e] & 0xffff0000u) + acc[f][j + 1]) << 16;
-                        } else o[e] = __float_as_uint(__uint_as_float(old[i].u[h][e]) + acc[h][e]);
-                    }
-                    ((u32x4 *)y)[h] = o;
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (e < mine) {
-                        const float v = acc[e >> 2][e & 3];
-                        if (BF16) ((uint16_t *)y)[e] = (uint16_t)to_bf16(bf16_bits_to_f32(((const uint16_t *)add)[e]) + v);
-                        else ((float *)y)[e] = ((const float *)add)[e] + v;
+                        for (int f = 0; f < 4; ++f) acc[f] = mfma16x16x32(__builtin_bit_cast(bf16x8, w[f][s]), x, acc[f]);
                     }
             }
+            // D: lane (r, g) holds rows 4 g + i of token r
+#pragma unroll
+            for (int h = 0; h < PW; ++h) {
+                const int mine = 16 * i + r < count ? min(PV, Np - n0 - at(h)) : 0;                    // outputs of this piece
+                const int64_t from = (int64_t)q * Np + n0 + at(h);
+                const char *const add = (const char *)p.add + ((int64_t)t[i] * p.ldadd + from) * ES;
+                char *const y = (char *)p.y + ((int64_t)t[i] * p.ldy + from) * ES;
+                if (VEC && mine == PV) {
+                    u32x4 o = old[i].u[h];
+                    if (tile.adapter >= 0) {     // else add as it is
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (BF16) {
+                                const int f = 2 * h + (e >> 1), j = 2 * (e & 1);
+                                o[e] = to_bf16(__uint_as_float(o[e] << 16) + acc[f][j]) |
+                                       to_bf16(__uint_as_float(o[e] & 0xffff0000u) + acc[f][j + 1]) << 16;
+                            } else o[e] = __float_as_uint(__uint_as_float(o[e]) + acc[h][e]);
+                        }
+                    }
+                    *(u32x4 *)y = o;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < PV; ++e)
+                        if (e < mine) {
+                            const float v = acc[BF16 ? 2 * h + (e >> 2) : h][e & 3];
+                            if (BF16) {
+                                const uint16_t a = ((const uint16_t *)add)[e];
+                                ((uint16_t *)y)[e] = tile.adapter < 0 ? a : (uint16_t)to_bf16(bf16_bits_to_f32(a) + v);
+                            } else {
+                                const uint32_t a = ((const uint32_t *)add)[e];
+                                ((uint32_t *)y)[e] = tile.adapter < 0 ? a : __float_as_uint(__uint_as_float(a) + v);
+                            }
+                        }
+                }
+            }
         }
+    }
+}
+
+// ---------------------------------------------------------------- down for large batches
+// Tiles of 64 tokens with aligned rows: x and A go to LDS without passing registers,
+// in steps of 128 bytes of K's x (64 bf16 or 64 codes and 32 fp32 values a row), three
+// steps deep.  Eight neighbouring lanes load a row's 128 bytes: in the layout of the
+// matrix instructions neighbouring lanes are different rows, and the cache then
+// serves one lane a cycle (8192 x 7168, rank 2 x 64: 89 us).  16-byte pieces are
+// stored at piece ^ key(row), for the banks.
+constexpr int RING = 3;
+
+template <int KIND>
+constexpr int step_k() { return KIND == ADAPT_F32 ? 32 : 64; }
+
+// FR: fragments of 16 columns, a power of two
+template <int FR, int KIND>
+__global__ __launch_bounds__(256) void adapter_down_wide(AdapterPass p, int k_parts)
+{
+    constexpr int NS = terms<KIND>(), SK = step_k<KIND>(), XROW = KIND == ADAPT_I8 ? 64 : 128, AROW = SK * 2;
+    constexpr int XB = 64 * XROW, AB = FR * 16 * AROW, LX = XB / 4096, LA = AB < 4096 ? 1 : AB / 4096;   // loads of a wave and step
+    constexpr int CW = FR >= 4 ? 4 : FR, TW = 4 / CW, CT = FR / CW, TT = 4 / TW;       // waves along columns and tokens, fragments of a wave
+    extern __shared__ __align__(16) int8_t ring[];                     // [RING][x, A]
+    const AdapterTile tile = p.tiles[blockIdx.x];
+    if (tile.adapter < 0) return;
+    const int count = min(64, p.offsets[tile.adapter + 1] - tile.begin);
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
+    const int R = p.parts * p.rank, r8 = (p.rank + 7) & ~7, width = p.parts * r8;
+    const int steps = (p.K + SK - 1) / SK, part = blockIdx.y;
+    const int s0 = (int)((int64_t)steps * part / k_parts), s1 = (int)((int64_t)steps * (part + 1) / k_parts);
+    constexpr int ES = KIND == ADAPT_F32 ? 4 : KIND == ADAPT_BF16 ? 2 : 1, STAGE = XB + AB;
+    constexpr int XP = XROW / 16, AP = AROW / 16;                      // pieces of a row
+    auto key = [](int row, int pieces) { return (row >> (pieces == 4 ? 1 : 0)) & (pieces - 1); };
+    // what this lane loads: piece (lane % pieces) ^ key of row (wave, load, lane / pieces)
+    const char *xp[LX];
+    int xk[LX];
+#pragma unroll
+    for (int i = 0; i < LX; ++i) {
+        const int row = ((wave * LX + i) * 64 + lane) / XP, piece = (lane % XP) ^ key(row, XP);
+        xp[i] = (const char *)p.x + (int64_t)p.order[tile.begin + min(row, count - 1)] * p.ldx * ES;
+        xk[i] = piece * (16 / ES);
+    }
+    const uint16_t *ap[LA];
+    int ak[LA];
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+        const int row = (((wave * LA + i) * 64 + lane) / AP) % (FR * 16), piece = (lane % AP) ^ key(row, AP);
+        ap[i] = p.a + ((int64_t)tile.adapter * R + min(row, R - 1)) * p.lda;
+        ak[i] = piece * 8;
+    }
+    const int last_x = p.K - 16 / ES, last_a = ((p.K + 7) & ~7) - 8;
+    auto fetch = [&](int s) {                    // past the end: the last step again, into a slot that nobody reads
+        int8_t *const at = ring + s % RING * STAGE;
+        const int k = SK * min(s, s1 - 1);
+#pragma unroll
+        for (int i = 0; i < LX; ++i)
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(xp[i] + (int64_t)min(k + xk[i], last_x) * ES),
+                                             (__attribute__((address_space(3))) void *)(at + (wave * LX + i) * 1024), 16, 0, 0);
+#pragma unroll
+        for (int i = 0; i < LA; ++i)
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(ap[i] + min(k + ak[i], last_a)),
+                                             (__attribute__((address_space(3))) void *)(at + XB + (wave * LA + i) * 1024 % AB), 16, 0, 0);
+    };
+    const int wc = wave % CW, wt = wave / CW;
+    f32x4 acc[TT][CT];
+#pragma unroll
+    for (int i = 0; i < TT; ++i)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[i][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    fetch(s0);
+    fetch(s0 + 1);
+    for (int s = s0; s < s1; ++s) {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt((LX + LA) | 0x70);                  // vmcnt: the next step may be on its way; lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();            // step s has landed for everybody, and step s - 1 is read
+        asm volatile("" ::: "memory");
+        fetch(s + 2);
+        const int8_t *const xb = ring + s % RING * STAGE, *const ab = xb + XB;
+#pragma unroll
+        for (int h = 0; h < SK / 32; ++h) {
+            const int k = 32 * h + 8 * g;        // of the step
+            u32x4 w[CT];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                const int row = 16 * (wc + CW * c) + r;
+                w[c] = *(const u32x4 *)(ab + row * AROW + 16 * ((k / 8) ^ key(row, AP)));
+                if (SK * s + k > last_a) w[c] = u32x4{0, 0, 0, 0};     // past K
+            }
+#pragma unroll
+            for (int i = 0; i < TT; ++i) {
+                const int row = 16 * (wt + TW * i) + r;
+                Raw v;
+                if (KIND == ADAPT_F32) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) v.u[q] = *(const u32x4 *)(xb + row * XROW + 16 * ((k / 4 + q) ^ key(row, XP)));
+                } else if (KIND == ADAPT_BF16) v.u[0] = *(const u32x4 *)(xb + row * XROW + 16 * ((k / 8) ^ key(row, XP)));
+                else {
+                    const uint2 c = *(const uint2 *)(xb + row * XROW + 16 * ((k / 16) ^ key(row, XP)) + (k & 8));
+                    v.u[0][0] = c.x;
+                    v.u[0][1] = c.y;
+                }
+                bf16x8 a[3];
+                as_terms<KIND>(v, a);
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+#pragma unroll
+                    for (int q = NS - 1; q >= 0; --q)                  // smallest term first
+                        acc[i][c] = mfma16x16x32(a[q], __builtin_bit_cast(bf16x8, w[c]), acc[i][c]);
+            }
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(0x0f70);          // no load may be in flight when the LDS is freed
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+        const int f = 16 * (wc + CW * c) + r;    // D: lane (r, g) holds tokens 4 g .. 4 g + 3 of column r
+        if (f >= R) continue;
+        float *const o = p.low + ((int64_t)part * p.T + tile.begin) * width + f / p.rank * r8 + f % p.rank;
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int t = 16 * (wt + TW * i) + 4 * g + q;
+                if (t < count) o[(int64_t)t * width] = acc[i][c][q];
+            }
     }
 }
 
@@ -507,8 +646,32 @@ hipError_t launch_adapter_down(const AdapterPass &p, hipStream_t s)
     // up to four column fragments a wave; the other waves divide K
     const int cw = frags <= 4 ? 1 : frags <= 8 ? 2 : 4, ct = (frags + cw - 1) / cw, waves = tt == 1 ? down_waves<1>() : down_waves<4>();
     const int es = p.kind == ADAPT_F32 ? 4 : p.kind == ADAPT_BF16 ? 2 : 1;
-    const bool vec = aligned(p.x, p.ldx, es, std::min(16, 8 * es));
+    const bool vec = aligned(p.x, p.ldx, es, std::min(16, 8 * es)) && p.K % 8 == 0;
     const dim3 grid((unsigned)adapter_tiles(p.T, p.n), (unsigned)parts);
+    // rows whose 16-byte pieces are aligned
+    if (tt == 4 && aligned(p.x, p.ldx, es, 16) && p.K % (16 / es) == 0) {
+#define MOE_WIDE2(fr, kind)                                                                       \
+    do {                                                                                          \
+        static DevSlots slots{};                                                                  \
+        const size_t ring = (size_t)RING * (64 * (kind == ADAPT_I8 ? 64 : 128) + fr * 16 * step_k<kind>() * 2); \
+        const hipError_t e = lds_limit((const void *)adapter_down_wide<fr, kind>, slots, ring);   \
+        if (e != hipSuccess) return e;                                                            \
+        adapter_down_wide<fr, kind><<<grid, 256, ring, s>>>(p, parts);                            \
+        return hipGetLastError();                                                                 \
+    } while (0)
+#define MOE_WIDE(fr)                                                                              \
+    do {                                                                                          \
+        if (p.kind == ADAPT_F32) MOE_WIDE2(fr, ADAPT_F32);                                        \
+        else if (p.kind == ADAPT_BF16) MOE_WIDE2(fr, ADAPT_BF16);                                 \
+        else MOE_WIDE2(fr, ADAPT_I8);                                                             \
+    } while (0)
+        if (frags <= 2) MOE_WIDE(2);
+        else if (frags <= 4) MOE_WIDE(4);
+        else if (frags <= 8) MOE_WIDE(8);
+        else MOE_WIDE(16);
+#undef MOE_WIDE
+#undef MOE_WIDE2
+    }
     const size_t lds = (size_t)(waves / cw / 2) * tt * frags * 64 * 16;
 #define MOE_DOWN3(t, c, kind, v)                                                                  \
     do {                                                                                          \
@@ -524,7 +687,8 @@ hipError_t launch_adapter_down(const AdapterPass &p, hipStream_t s)
     } while (0)
 #define MOE_DOWN1(t, kind)                                                                        \
     do {                                                                                          \
-        if (ct <= 2) MOE_DOWN2(t, 2, kind);                                                       \
+        if (ct == 1) MOE_DOWN2(t, 1, kind);                                                       \
+        else if (ct == 2) MOE_DOWN2(t, 2, kind);                                                       \
         else MOE_DOWN2(t, 4, kind);                                                               \
     } while (0)
 #define MOE_DOWN(t)                                                                               \
@@ -547,7 +711,7 @@ hipError_t launch_adapter_up(const AdapterPass &p, hipStream_t s)
     const int parts = adapter_k_parts(p.T, p.K, p.n), es = p.y_bf16 ? 2 : 4;
     const int tiles = adapter_tiles(p.T, p.n), groups = (p.N / p.parts + WIDE - 1) / WIDE;
     // about 16 waves a CU, stretches of at least a group a wave
-    const int chunks = std::max(1, std::min((groups + 3) / 4, (1024 + tiles * p.parts - 1) / (tiles * p.parts)));
+    const int chunks = std::max(1, std::min((groups + 3) / 4, (512 + tiles * p.parts - 1) / (tiles * p.parts)));
     const bool vec = aligned(p.y, p.ldy, es, 16) && aligned(p.add, p.ldadd, es, 16) && p.N / p.parts % (16 / es) == 0;
     const dim3 grid((unsigned)tiles, (unsigned)(p.parts * chunks));
 #define MOE_UP3(t, bf, v)                                                                         \
