@@ -671,14 +671,11 @@ class AdapterWeights:
     def _rows(t):
         import torch
         n, rows, k = t.shape
-        ld = (k + 7) // 8 * 8
-        if ld > 256:
-            ld = (ld + 127) // 128 * 128 + 64
-        if k % 8 == 0 and ld == k and t.is_contiguous() and t.data_ptr() % 16 == 0:
+        if k % 8 == 0 and t.is_contiguous() and t.data_ptr() % 16 == 0:
             return t
-        out = torch.zeros((n, rows, ld), dtype=t.dtype, device=t.device)
+        out = torch.zeros((n, rows, (k + 7) // 8 * 8), dtype=t.dtype, device=t.device)
         out[:, :, :k] = t
-        return out[:, :, :(k + 7) // 8 * 8]
+        return out
 
     def workspace(self, T: int, device="cuda"):
         """A workspace for up to T tokens."""

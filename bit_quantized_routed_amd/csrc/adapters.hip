@@ -294,9 +294,9 @@ __global__ __launch_bounds__(64 * down_waves<TT>()) void adapter_down(AdapterPas
         Step even, odd;
         load(s0, even);
         for (int s = s0; s < s1; s += 2) {
-            load(s + 1, odd);
+            if (s + 1 < s1) load(s + 1, odd);
             multiply(s, even);
-            load(s + 2, even);
+            if (s + 2 < s1) load(s + 2, even);
             if (s + 1 < s1) multiply(s + 1, odd);
         }
     }
@@ -340,14 +340,30 @@ __global__ __launch_bounds__(64 * down_waves<TT>()) void adapter_down(AdapterPas
 // ---------------------------------------------------------------- up: y = add + scale B low
 // A work-group takes a tile (TT fragments of 16 tokens) and a stretch of one part's
 // outputs.  low, with its scale and as bf16 terms, is made once in LDS; each of the
-// four waves then takes 64 outputs at a time: four fragments whose rows are dealt so
-// that a lane's outputs are 16-byte pieces of one token and four lanes hold 64 bytes
-// in a row (with 16 outputs in a row a lane, every lane of a store was a segment of
-// its own: 512 x 7168 from rank 32 took 16 us).
+// four waves then takes 64 outputs at a time: fragment f has outputs f, f + 4, .. of
+// them, so that a lane ends up with four outputs in a row and 16 neighbouring lanes
+// with the 64 of one token (with a token a lane the cache served one lane a cycle:
+// 8192 x 4096 of bf16 54 us).
 constexpr int WIDE = 64;
 
 template <bool BF16>
-struct Piece { u32x4 u[BF16 ? 2 : 4]; };         // 16 values
+struct Four { uint32_t u[BF16 ? 2 : 4]; };       // four outputs
+
+template <bool BF16>
+__device__ __forceinline__ Four<BF16> load_four(const void *p)
+{
+    Four<BF16> v;
+    if (BF16) {
+        const uint2 u = *(const uint2 *)p;
+        v.u[0] = u.x;
+        v.u[1] = u.y;
+    } else {
+        const u32x4 u = *(const u32x4 *)p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v.u[BF16 ? 0 : i] = u[i];
+    }
+    return v;
+}
 
 template <int TT, bool BF16, bool VEC, int KS>   // KS: steps of 32 of the rank
 __global__ __launch_bounds__(256) void adapter_up(AdapterPass p, int k_parts, int chunks)
@@ -359,42 +375,41 @@ __global__ __launch_bounds__(256) void adapter_up(AdapterPass p, int k_parts, in
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const int Np = p.N / p.parts, groups = (Np + WIDE - 1) / WIDE, r8 = (p.rank + 7) & ~7, width = p.parts * r8;
     const int q = blockIdx.y / chunks, chunk = blockIdx.y % chunks, u1 = groups * (chunk + 1) / chunks;
-    // a lane's piece h: PV outputs from n0 + at(h) on
-    constexpr int ES = BF16 ? 2 : 4, PW = BF16 ? 2 : 4, PV = 16 / PW;
-    auto at = [&](int h) { return 4 * PV * h + PV * g; };
-    int t[TT];
+    constexpr int ES = BF16 ? 2 : 4;
+    int t[TT][4];                                // tokens 4 g .. 4 g + 3 of each fragment
 #pragma unroll
-    for (int i = 0; i < TT; ++i) t[i] = p.order[tile.begin + min(16 * i + r, count - 1)];
-    // what a group of 64 outputs reads: b's rows of this lane (the outputs of fragment f, zero past the rank) and add; the first group's are on their way while low is made
-    u32x4 w[4][KS];
-    Piece<BF16> old[TT];
-    auto load = [&](int u) {
+    for (int i = 0; i < TT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[i][e] = p.order[tile.begin + min(16 * i + 4 * g + e, count - 1)];
+    // what a group of 64 outputs reads: b's rows of this lane and add; the first group's are on their way while low is made.  No
+    // branches: what lies past the end is clamped, and not stored; past the rank low is zero
+    struct Group { u32x4 w[4][KS]; Four<BF16> old[TT][4]; };
+    auto load = [&](int u, Group &v) {
         const int n0 = min(u, groups - 1) * WIDE;
-        // no branches: what lies past the end is clamped, and not stored; past the rank low is zero
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
-            const int n = min(n0 + (BF16 ? 32 * (f >> 1) + 8 * (r >> 2) + 4 * (f & 1) + (r & 3) : 16 * f + r), Np - 1);
-            const uint16_t *const row = p.b + ((int64_t)max(tile.adapter, 0) * p.N + (int64_t)q * Np + n) * p.ldb;
+            const uint16_t *const row = p.b + ((int64_t)max(tile.adapter, 0) * p.N + (int64_t)q * Np + min(n0 + 4 * r + f, Np - 1)) * p.ldb;
 #pragma unroll
-            for (int s = 0; s < KS; ++s) w[f][s] = *(const u32x4 *)(row + min(32 * s + 8 * g, r8 - 8));
+            for (int s = 0; s < KS; ++s) v.w[f][s] = *(const u32x4 *)(row + min(32 * s + 8 * g, r8 - 8));
         }
         if (VEC) {
 #pragma unroll
             for (int i = 0; i < TT; ++i)
 #pragma unroll
-                for (int h = 0; h < PW; ++h)
-                    old[i].u[h] = *(const u32x4 *)((const char *)p.add + ((int64_t)t[i] * p.ldadd + (int64_t)q * Np + min(n0 + at(h), Np - PV)) * ES);
+                for (int e = 0; e < 4; ++e)
+                    v.old[i][e] = load_four<BF16>((const char *)p.add + ((int64_t)t[i][e] * p.ldadd + (int64_t)q * Np + min(n0 + 4 * r, Np - 4)) * ES);
         }
     };
     const int u0 = groups * chunk / chunks + wave;
-    load(u0);
+    Group even, odd;
+    load(u0, even);
     if (tile.adapter >= 0) {
         const float scale = p.scale[tile.adapter];
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
             if (i % 4 != wave) continue;
             const int pos = tile.begin + min(16 * i + r, count - 1);
-            const float factor = scale * (p.x_scale ? p.x_scale[t[i]] : 1.0f);
+            const float factor = scale * (p.x_scale ? p.x_scale[p.order[pos]] : 1.0f);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 // the parts of K in order, eight parts' loads on their way together
@@ -427,12 +442,11 @@ __global__ __launch_bounds__(256) void adapter_up(AdapterPass p, int k_parts, in
         }
         __syncthreads();
     }
-    for (int u = u0; u < u1; u += 4) {
-        if (u > u0) load(u);
-        const int n0 = u * WIDE;
+    auto finish = [&](int u, const Group &v) {
+        const int n0 = u * WIDE, mine = min(4, Np - n0 - 4 * r);       // outputs of this lane (none if negative)
+        const int64_t from = (int64_t)q * Np + n0 + 4 * r;
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
-            if (TT == 1 && 16 * i >= count) break;
             f32x4 acc[4];
 #pragma unroll
             for (int f = 0; f < 4; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -443,45 +457,52 @@ __global__ __launch_bounds__(256) void adapter_up(AdapterPass p, int k_parts, in
                     for (int s = 0; s < KS; ++s) {
                         const bf16x8 x = low[m][i][s][lane];
 #pragma unroll
-                        for (int f = 0; f < 4; ++f) acc[f] = mfma16x16x32(__builtin_bit_cast(bf16x8, w[f][s]), x, acc[f]);
+                        for (int f = 0; f < 4; ++f) acc[f] = mfma16x16x32(x, __builtin_bit_cast(bf16x8, v.w[f][s]), acc[f]);
                     }
             }
-            // D: lane (r, g) holds rows 4 g + i of token r
+            // D: lane (r, g) holds tokens 4 g + e of output 4 r + f
 #pragma unroll
-            for (int h = 0; h < PW; ++h) {
-                const int mine = 16 * i + r < count ? min(PV, Np - n0 - at(h)) : 0;                    // outputs of this piece
-                const int64_t from = (int64_t)q * Np + n0 + at(h);
-                const char *const add = (const char *)p.add + ((int64_t)t[i] * p.ldadd + from) * ES;
-                char *const y = (char *)p.y + ((int64_t)t[i] * p.ldy + from) * ES;
-                if (VEC && mine == PV) {
-                    u32x4 o = old[i].u[h];
+            for (int e = 0; e < 4; ++e) {
+                if (16 * i + 4 * g + e >= count) continue;
+                const char *const add = (const char *)p.add + ((int64_t)t[i][e] * p.ldadd + from) * ES;
+                char *const y = (char *)p.y + ((int64_t)t[i][e] * p.ldy + from) * ES;
+                if (VEC && mine == 4) {
+                    Four<BF16> o = v.old[i][e];
                     if (tile.adapter >= 0) {     // else add as it is
+                        if (BF16) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (BF16) {
-                                const int f = 2 * h + (e >> 1), j = 2 * (e & 1);
-                                o[e] = to_bf16(__uint_as_float(o[e] << 16) + acc[f][j]) |
-                                       to_bf16(__uint_as_float(o[e] & 0xffff0000u) + acc[f][j + 1]) << 16;
-                            } else o[e] = __float_as_uint(__uint_as_float(o[e]) + acc[h][e]);
+                            for (int j = 0; j < 2; ++j)
+                                o.u[j] = to_bf16(__uint_as_float(o.u[j] << 16) + acc[2 * j][e]) |
+                                         to_bf16(__uint_as_float(o.u[j] & 0xffff0000u) + acc[2 * j + 1][e]) << 16;
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) o.u[BF16 ? 0 : j] = __float_as_uint(__uint_as_float(o.u[BF16 ? 0 : j]) + acc[j][e]);
                         }
                     }
-                    *(u32x4 *)y = o;
+                    if (BF16) *(uint2 *)y = uint2{o.u[0], o.u[1]};
+                    else *(u32x4 *)y = u32x4{o.u[0], o.u[1], o.u[BF16 ? 0 : 2], o.u[BF16 ? 0 : 3]};
                 } else {
 #pragma unroll
-                    for (int e = 0; e < PV; ++e)
-                        if (e < mine) {
-                            const float v = acc[BF16 ? 2 * h + (e >> 2) : h][e & 3];
+                    for (int f = 0; f < 4; ++f)
+                        if (f < mine) {
                             if (BF16) {
-                                const uint16_t a = ((const uint16_t *)add)[e];
-                                ((uint16_t *)y)[e] = tile.adapter < 0 ? a : (uint16_t)to_bf16(bf16_bits_to_f32(a) + v);
+                                const uint16_t a = ((const uint16_t *)add)[f];
+                                ((uint16_t *)y)[f] = tile.adapter < 0 ? a : (uint16_t)to_bf16(bf16_bits_to_f32(a) + acc[f][e]);
                             } else {
-                                const uint32_t a = ((const uint32_t *)add)[e];
-                                ((uint32_t *)y)[e] = tile.adapter < 0 ? a : __float_as_uint(__uint_as_float(a) + v);
+                                const uint32_t a = ((const uint32_t *)add)[f];
+                                ((uint32_t *)y)[f] = tile.adapter < 0 ? a : __float_as_uint(__uint_as_float(a) + acc[f][e]);
                             }
                         }
                 }
             }
         }
+    };
+    // two groups by name: a copy of the one would wait for its loads
+    for (int u = u0; u < u1; u += 8) {
+        if (u + 4 < u1) load(u + 4, odd);
+        finish(u, even);
+        if (u + 8 < u1) load(u + 8, even);
+        if (u + 4 < u1) finish(u + 4, odd);
     }
 }
 
@@ -710,9 +731,9 @@ hipError_t launch_adapter_up(const AdapterPass &p, hipStream_t s)
 {
     const int parts = adapter_k_parts(p.T, p.K, p.n), es = p.y_bf16 ? 2 : 4;
     const int tiles = adapter_tiles(p.T, p.n), groups = (p.N / p.parts + WIDE - 1) / WIDE;
-    // about 16 waves a CU, stretches of at least a group a wave
+    // about two work-groups a CU, stretches of at least a group a wave
     const int chunks = std::max(1, std::min((groups + 3) / 4, (512 + tiles * p.parts - 1) / (tiles * p.parts)));
-    const bool vec = aligned(p.y, p.ldy, es, 16) && aligned(p.add, p.ldadd, es, 16) && p.N / p.parts % (16 / es) == 0;
+    const bool vec = aligned(p.y, p.ldy, es, 4 * es) && aligned(p.add, p.ldadd, es, 4 * es) && p.N / p.parts % 4 == 0;
     const dim3 grid((unsigned)tiles, (unsigned)(p.parts * chunks));
 #define MOE_UP3(t, bf, v)                                                                         \
     do {                                                                                          \
