@@ -615,6 +615,10 @@ class BlockWeights:
                         (_ACTS or _acts())[torch.bfloat16 if act is None else act])
         self.ref = ctypes.byref(self.c)
 
+    def takes(self, T: int) -> bool:
+        """Whether moe_block_decode takes these weights and T tokens."""
+        return int(lib().moe_block_decode_workspace_bytes(self.ref, T)) > 0
+
     def workspace(self, T: int, device="cuda"):
         """A workspace for up to T tokens, for calls that do not overlap in time."""
         import torch

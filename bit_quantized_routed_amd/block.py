@@ -67,12 +67,8 @@ class MoeBlock:
                              % (gate_up.out_features, gate_up.in_features, down.out_features, down.in_features, self.hidden))
         if (router.hidden, router.n_experts, router.top_k) != (layer.hidden, layer.n_experts, layer.top_k):
             raise ValueError("router and layer differ in hidden, experts or top k")
-        self.few = M.BlockWeights(norm, router, layer, gate_up, down) if self._takes_few(layer.c) else None
-
-    def _takes_few(self, c):
-        """Whether moe_block_decode takes these weights."""
-        return ((c.fmt_gate_up, c.fmt_down) == (M.FMT_CB2, M.FMT_Q2K) and not c.flags and not c.expert_slot
-                and max(c.hidden, c.inter, self.sh_inter) <= 8192 and c.n_experts <= 512 and c.top_k <= 16)
+        few = M.BlockWeights(norm, router, layer, gate_up, down)
+        self.few = few if few.takes(1) else None
 
     def decode(self, x, residual, b: BlockBuffers, stream=None):
         """The block for up to 16 tokens in two kernels (see moe_block_decode).  x, residual: [T, H] rows; residual is updated in

@@ -479,7 +479,7 @@ size_t moe_linear_i8_workspace_bytes(const moe_linear *W, int T);
  * where it stands for moe_residual_norm, moe_route_scored, moe_expert_ffn_decode and the
  * shared expert's int8 linear layers.  Weights are applied exactly and activations with an
  * error of 2^-24 of the largest value of their 256 neighbours, sums are exact within 256
- * products and fp32 beyond: y is within a few 2^-22 relative of 64-bit arithmetic on the
+ * products and fp32 beyond: y is within about 4e-7 (2-norm) of 64-bit arithmetic on the
  * same n.  The shared expert's activations are not cut to 8 bits here, so its output
  * differs from that of moe_linear_i8 on codes by those codes' rounding.  A token's y
  * depends on the rest of the batch only in the order of fp32 sums.
@@ -490,7 +490,8 @@ size_t moe_linear_i8_workspace_bytes(const moe_linear *W, int T);
  *     [gate | up], down [H][I_s]; biases are added.
  *   hidden and inter are multiples of 8; hidden, inter and I_s at most 8192, E at most 512, k
  *     at most 16, T at most 16 (MOE_ERR_UNSUPPORTED otherwise).
- * x and residual rows, sum and ws 16-byte aligned, strides multiples of 8 elements; sum: NULL
+ * x and residual rows, sum, ws and the norm's weight 16-byte aligned, strides multiples of 8
+ * elements; sum: NULL
  * or the residual's type, may be the residual; y may be x.  Nothing else may overlap.  A workspace of
  * moe_block_decode_workspace_bytes() for T tokens serves every smaller batch and needs no
  * clearing, but calls that may overlap in time (two streams, two graphs) need one each: the
