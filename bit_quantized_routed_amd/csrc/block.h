@@ -31,7 +31,7 @@ struct BlockPass {
     int32_t *list;                               // different experts, then a token and a weight for each position
     double *logits;                              // [T][E]
     void *s;                                     // [T][H] of the residual's type
-    int8_t *planes;                              // [T][quads of H][3072]
+    int8_t *planes;                              // [T][quads of H][digits of four blocks]
     float *scales;                               // [T][4 quads of H]
     int8_t *h;                                   // [T k][records] of 64 features in digits
     float *hs;                                   // [T][sh]

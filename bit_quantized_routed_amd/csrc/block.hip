@@ -7,11 +7,11 @@
 // else: its work is cut into items (the selection, 8 features of the shared
 // gate/up, F features of a routed expert's gate/up, some rows of y) that
 // work-groups draw by ticket, in that order, and an item waits only for items of
-// lower tickets: for the selection, for h of all experts.  Tickets are drawn by running work-groups only, so the lowest
-// unfinished item is always being worked on and every wait ends, however many
-// work-groups are resident and whatever else runs on the device.  (A bound on
-// the polls ends a wait all the same, should a second call overwrite the
-// workspace; y is NaN then.)
+// lower tickets: for the selection, for h of all experts.  Tickets are drawn by
+// running work-groups only, so the lowest unfinished item is always being worked
+// on and every wait ends, however many work-groups are resident and whatever else
+// runs on the device.  (A bound on the polls ends a wait all the same, should a
+// second call overwrite the workspace; y is NaN then.)
 //
 // Data that a work-group hands to others goes past its XCD's cache (agent-scope
 // stores; the arrival counter is raised after they are acknowledged).
@@ -29,6 +29,18 @@
 // four blocks x (three digits and a spare), zero where a lane's block is another
 // one: sums of different blocks never mix, and each arrives in the lane that holds
 // the block's scale.
+//
+// What bounds it.  Its floor is the weights of the experts that the tokens chose,
+// but the parts stand in a row and each has its latency: one token, H 7168, I 2048,
+// 8 of 256 experts and a shared one, 125 MB: 50 us (2.5 TB/s; a large copy reaches
+// 5.1): 10.6 until the experts are known (the shared gate/up runs beside it), 12 of
+// routed gate/up (of that 5 more than its loads need, for the codewords' products),
+// 9 until every h is there, 9 of rows of y, and the drain.  Four such tokens, 332 MB:
+// 126 us (2.6 TB/s).  Sixteen of a small layer (H 2048, I 768, 6 of 64), 60 MB: 94 us,
+// bound by the arithmetic, which is done for each pair of a token and an expert.  The
+// norm before it: 7, 12 and 9 us.  One work-group a CU of eight waves, because the
+// tables and digits take most of the LDS and the products up to 256 registers (the
+// same with 12 waves 65 us and with 16, which spill, 80, when this took 62).
 #include "block.h"
 #include "common.h"
 #include "devcache.h"
@@ -47,8 +59,8 @@ typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(4)));
 
 constexpr int NORM_NT = 1024, NORM_NW = NORM_NT / 64;
 constexpr int NT = 512, NW = NT / 64;
-constexpr int QUAD = 3072;                       // bytes of four blocks' digits: [16 steps][4 blocks][3 digits][16]
-constexpr float QMAX = 8323072.0f;               // 127 * 2^16
+constexpr int QUAD = 16 * 4 * 3 * 16;            // bytes of four blocks' digits: [16 steps][4 blocks][3 digits][16]
+constexpr float QMAX = 127.0f * 65536.0f;
 // 64 features of a row of h: [4 steps][3 digits][16] in the order of Q2_K's codes (dword i of a step = features i, i + 4, i + 8,
 // i + 12), the sums of the four steps (fp32) and the scale.  A record has lines of its own in the workspace; in LDS four
 // records are a block's, a little apart from the next block's for the banks' sake.
@@ -402,7 +414,7 @@ __device__ __noinline__ void select(Args pa)
     if (tid == 0) post(p.ctl + C_LIST, (uint32_t)all);
 }
 
-// ---- 8 features of the shared gate/up: a tile of rows gate f .. f + 7, up f .. f + 7; a wave's blocks of K are wave, wave + 16, ..
+// ---- 8 features of the shared gate/up: a tile of rows gate f .. f + 7, up f .. f + 7; the waves take the blocks of K in turn
 __device__ __forceinline__ const int8_t *digit_base(const BlockPass &p, bool in, int slot, int stride, int at)
 {
     return in ? smem + p.o_planes + slot * stride + at : smem + O_ZERO;
@@ -639,7 +651,9 @@ __device__ __forceinline__ void stage_shared(const BlockPass &p, int t0, int cou
     }
 }
 
-// Records of `count` rows of h from c0 on into LDS; what no item has written (past inter) is zero.
+// Records of `count` rows of h from c0 on into LDS; what no item has written (past inter) is zero.  Plain loads: a record's lines
+// hold nothing else, and no cache can have an older copy, since this kernel reads them here alone, after their item has counted
+// itself in, and the caches were emptied at its start.
 __device__ __forceinline__ void stage_h(const BlockPass &p, int c0, int count)
 {
     constexpr int PIECES = REC / 16;

@@ -491,11 +491,11 @@ size_t moe_linear_i8_workspace_bytes(const moe_linear *W, int T);
  *   hidden and inter are multiples of 8; hidden, inter and I_s at most 8192, E at most 512, k
  *     at most 16, T at most 16 (MOE_ERR_UNSUPPORTED otherwise).
  * x and residual rows, sum, ws and the norm's weight 16-byte aligned, strides multiples of 8
- * elements; sum: NULL
- * or the residual's type, may be the residual; y may be x.  Nothing else may overlap.  A workspace of
- * moe_block_decode_workspace_bytes() for T tokens serves every smaller batch and needs no
- * clearing, but calls that may overlap in time (two streams, two graphs) need one each: the
- * call's counters are in it.  (Shared all the same, the calls end and y is wrong or NaN.) */
+ * elements; sum: NULL or the residual's type, may be the residual; y may be x.  Nothing else
+ * may overlap.  A workspace of moe_block_decode_workspace_bytes() for T tokens serves every
+ * smaller batch and needs no clearing, but calls that may overlap in time (two streams, two
+ * graphs) need one each: the call's counters are in it.  (Shared all the same, the calls end
+ * and y is wrong or NaN.) */
 typedef struct moe_block {
     const moe_norm *norm;
     const moe_router *router;
