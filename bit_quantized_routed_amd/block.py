@@ -24,7 +24,8 @@ FEW_TOKENS = 16
 
 class StepAdapters:
     """The adapters of one step at one block: the step's plan (M.AdapterPlan, filled by M.adapter_plan) and the weights beside
-    the shared expert's gate/up rows (two parts) and its down rows, either of them None."""
+    the shared expert's gate/up rows (two parts) and its down rows, either of them None.  Blocks that run one after another may
+    share one; steps in flight at the same time need one each."""
 
     def __init__(self, plan, gate_up=None, down=None, device="cuda"):
         self.plan, self.gate_up, self.down = plan, gate_up, down
