@@ -652,8 +652,8 @@ __device__ __forceinline__ void stage_shared(const BlockPass &p, int t0, int cou
 }
 
 // Records of `count` rows of h from c0 on into LDS; what no item has written (past inter) is zero.  Plain loads: a record's lines
-// hold nothing else, and no cache can have an older copy, since this kernel reads them here alone, after their item has counted
-// itself in, and the caches were emptied at its start.
+// hold nothing else (block_workspace), and no cache can have an older copy, since this kernel reads them here alone, after their
+// item has counted itself in, and the caches were emptied at its start.
 __device__ __forceinline__ void stage_h(const BlockPass &p, int c0, int count)
 {
     constexpr int PIECES = REC / 16;
@@ -997,8 +997,13 @@ void block_layout(BlockPass &p)
     p.lds = O_END + area + red;
 }
 
+// Every piece begins on cache lines of its own, so from a multiple of 256 on, wherever the caller's workspace begins: h is
+// read with plain loads, and a line that holds anything a work-group has read earlier would come from its cache.  Returns the
+// bytes from `base` on.
 size_t block_workspace(BlockPass &p, char *base)
 {
+    const size_t gap = -(uintptr_t)base & 255;
+    base += gap;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         char *at = base + off;
@@ -1013,7 +1018,7 @@ size_t block_workspace(BlockPass &p, char *base)
     p.scales = (float *)take((size_t)p.T * 4 * p.nq * 4);
     p.h = (int8_t *)take((size_t)p.T * p.k * p.records * REC_LINES);
     p.hs = (float *)take((size_t)p.T * p.sh * 4);
-    return off;
+    return gap + off;
 }
 
 hipError_t launch_block_norm(const BlockPass &p, hipStream_t s)

@@ -277,7 +277,7 @@ size_t moe_block_decode_workspace_bytes(const moe_block *B, int T)
     BlockPass p{};
     if (T < 0 || check_block(B, T, p)) return 0;
     block_layout(p);
-    return block_workspace(p, nullptr);
+    return block_workspace(p, nullptr) + 240;    // from any multiple of 16 to the next of 256
 }
 
 int moe_block_decode(const moe_block *B, int T, const void *x, int act_x, int64_t ldx, const void *residual, int act_res,
