@@ -668,11 +668,12 @@ class AdapterWeights:
                              % (a.dtype, tuple(a.shape), b.dtype, tuple(b.shape), parts))
         self.a, self.b, self.scale = self._rows(a), self._rows(b), _vector(scale, n, "scale")
         self.in_features, self.out_features, self.n_adapters, self.rank, self.parts = K, N, n, r, parts
-        self.c = AdapterSetC(K, N, n, r, parts, self.a.stride(1), self.b.stride(1), _ptr(self.a), _ptr(self.b), _ptr(scale))
+        self.c = AdapterSetC(K, N, n, r, parts, self.a.shape[2], self.b.shape[2], _ptr(self.a), _ptr(self.b), _ptr(scale))
         self.ref = ctypes.byref(self.c)
 
     @staticmethod
     def _rows(t):
+        """t, or a copy, with rows of a multiple of 8 elements one after another (a matrix of one row may have any stride there)."""
         import torch
         n, rows, k = t.shape
         if k % 8 == 0 and t.is_contiguous() and t.data_ptr() % 16 == 0:
