@@ -692,7 +692,8 @@ class AdapterWeights:
 
 
 class AdapterPlan:
-    """Buffers of the plan for T tokens of n_adapters adapters (see adapter_plan)."""
+    """Buffers of the plan for T tokens of n_adapters adapters (see adapter_plan).  Before the first adapter_plan it holds no
+    tiles, and adapters() leaves y as it is."""
 
     def __init__(self, T: int, n_adapters: int, device="cuda"):
         import torch
@@ -701,7 +702,8 @@ class AdapterPlan:
         if T and tiles == 0:
             raise ValueError("no plan for %d tokens of %d adapters" % (T, n_adapters))
         self.T, self.n_adapters = T, n_adapters
-        self.order, self.offsets, self.tiles = torch.empty(T, **i32), torch.empty(n_adapters + 1, **i32), torch.empty((tiles, 2), **i32)
+        self.order, self.offsets = torch.empty(T, **i32), torch.empty(n_adapters + 1, **i32)
+        self.tiles = torch.full((tiles, 2), -2, **i32)                 # -2: no tile; what empty() leaves would be taken as indices
 
 
 def adapter_plan(ids, plan: AdapterPlan, stream=None, prof=None):

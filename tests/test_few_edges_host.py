@@ -36,3 +36,10 @@ def test_adapter_rows_of_one():
     assert (w.c.lda, w.c.ldb) == (K, r)
     w = M.AdapterWeights(torch.zeros(n, 5, 63, dtype=BF16), torch.zeros(n, 1, r, dtype=BF16)[:, :, :5], scale)       # copied
     assert (w.c.lda, w.c.ldb) == (64, 8)
+
+
+def test_plan_before_it_is_filled():
+    """A plan that no call has filled yet holds no tiles: the kernels take nothing from it."""
+    for T, n in ((1, 1), (512, 1024), (513, 3), (8192, 100)):
+        plan = M.AdapterPlan(T, n, device="cpu")
+        assert plan.tiles.shape == (M.lib().moe_adapter_tiles(T, n), 2) and torch.all(plan.tiles[:, 0] == -2)
