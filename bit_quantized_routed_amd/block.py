@@ -32,6 +32,15 @@ class StepAdapters:
         sizes = [w.workspace(plan.T, device) for w in (gate_up, down) if w is not None]
         self.ws = max(sizes, key=lambda t: t.nbytes) if sizes else None
 
+    def check(self, block: "MoeBlock", T: int):
+        """Raises ValueError unless this is a step of T tokens and fits the block."""
+        if self.plan.T != T:
+            raise ValueError("adapters: a plan of %d tokens, a step of %d" % (self.plan.T, T))
+        for name, w, K, N in (("gate_up", self.gate_up, block.hidden, 2 * block.sh_inter), ("down", self.down, block.sh_inter, block.hidden)):
+            if w is not None and (w.in_features, w.out_features, w.n_adapters) != (K, N, self.plan.n_adapters):
+                raise ValueError("adapters: %s of %d, %d x %d beside %d x %d, in a plan of %d"
+                                 % (name, w.n_adapters, w.out_features, w.in_features, N, K, self.plan.n_adapters))
+
 
 class BlockBuffers:
     """What one block writes for T tokens; blocks that run one after another may share one."""
@@ -82,6 +91,8 @@ class MoeBlock:
 
     def __call__(self, x, residual, b: BlockBuffers, stream=None, adapters: StepAdapters | None = None):
         """x, residual: [T, H] rows; residual is updated in place.  Returns b.y."""
+        if adapters is not None:
+            adapters.check(self, b.T)            # before the first launch changes the residual
         M.residual_norm(self.norm, x, residual, residual, b.n, b.q, b.q_scale, stream)
         M.route_scored(self.router, b.n, b.routing, b.ws_route, stream)
         ffn = M.ffn_decode if b.path == M.PATH_DECODE else M.ffn_prefill

@@ -1,6 +1,7 @@
 """Edges of the operators for a few tokens that need no GPU: what is checked, kept or sized before any launch."""
 import ctypes
 
+import pytest
 import torch
 
 import bit_quantized_routed_amd as M
@@ -43,3 +44,48 @@ def test_plan_before_it_is_filled():
     for T, n in ((1, 1), (512, 1024), (513, 3), (8192, 100)):
         plan = M.AdapterPlan(T, n, device="cpu")
         assert plan.tiles.shape == (M.lib().moe_adapter_tiles(T, n), 2) and torch.all(plan.tiles[:, 0] == -2)
+
+
+class Launched(Exception):
+    pass
+
+
+def _stub_block(monkeypatch, H, I, T):
+    """A block whose first launch is recorded and ends the call, and buffers for T tokens."""
+    from types import SimpleNamespace
+    from bit_quantized_routed_amd.block import MoeBlock
+    block, calls = object.__new__(MoeBlock), []
+    block.norm, block.hidden, block.sh_inter = None, H, I
+
+    def norm(*a):
+        calls.append("norm")
+        raise Launched
+
+    monkeypatch.setattr(M, "residual_norm", norm)
+    return block, SimpleNamespace(T=T, n=None, q=None, q_scale=None), calls
+
+
+@pytest.mark.parametrize("case", ["tokens", "adapters", "gate_up in", "gate_up out", "down in", "down out"])
+def test_step_adapters_that_do_not_fit(case, monkeypatch):
+    """Adapters of another step or block are refused before anything runs: the residual is updated in place."""
+    from bit_quantized_routed_amd.block import StepAdapters
+    H, I, T, n = 64, 32, 6, 3
+    block, b, calls = _stub_block(monkeypatch, H, I, T)
+
+    def weights(K, N, parts):
+        return M.AdapterWeights(torch.zeros(n, 8 * parts, K, dtype=BF16), torch.zeros(n, N, 8, dtype=BF16), torch.ones(n), parts)
+
+    def step(plan=None, gate_up=(H, 2 * I, 2), down=(I, H, 1)):
+        plan = M.AdapterPlan(T, n, device="cpu") if plan is None else plan
+        return StepAdapters(plan, None if gate_up is None else weights(*gate_up), None if down is None else weights(*down), device="cpu")
+
+    for good in (None, step(), step(gate_up=None), step(down=None), step(gate_up=(H, 2 * I, 1))):
+        with pytest.raises(Launched):
+            block(None, None, b, None, good)
+    assert len(calls) == 5
+    bad = {"tokens": lambda: step(M.AdapterPlan(T + 1, n, device="cpu")), "adapters": lambda: step(M.AdapterPlan(T, n + 1, device="cpu")),
+           "gate_up in": lambda: step(gate_up=(H + 8, 2 * I, 2)), "gate_up out": lambda: step(gate_up=(H, 2 * I + 2, 2)),
+           "down in": lambda: step(down=(I + 8, H, 1)), "down out": lambda: step(down=(I, H + 1, 1))}[case]
+    with pytest.raises(ValueError):
+        block(None, None, b, None, bad())
+    assert len(calls) == 5
