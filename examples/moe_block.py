@@ -13,7 +13,7 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import bit_quantized_routed_amd as M  # noqa: E402
 import synthetic as S  # noqa: E402
-from bit_quantized_routed_amd.block import FEW_TOKENS, BlockBuffers, MoeBlock  # noqa: E402
+from bit_quantized_routed_amd.block import BlockBuffers, MoeBlock  # noqa: E402
 from workload import Workload  # noqa: E402
 
 
@@ -56,7 +56,7 @@ def main(argv=None):
     (M.ffn_decode if b.path == M.PATH_DECODE else M.ffn_prefill)(block.layer, b.n, M.ACT_BF16, a.tokens, b.routing, routed, b.ws_ffn)
     want = plain_shared(b.n, gate_up, down)
     off = float((b.y.double() - routed.double() - want).norm() / want.norm())
-    if a.tokens <= FEW_TOKENS:                   # the same block in two kernels
+    if b.ws_few is not None:                     # the same block in two kernels
         few = block.decode(x, residual.clone(), BlockBuffers(block, a.tokens)).double()
         print("in two kernels: within %.2g%% of the operators one after the other"
               % (100 * float((few - b.y.double()).norm() / b.y.double().norm())), flush=True)

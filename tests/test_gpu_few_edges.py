@@ -29,3 +29,14 @@ def test_block_workspace_anywhere(T, H, I, sh, at):
         torch.cuda.synchronize()
         assert torch.equal(y, want) and torch.equal(r.topk_idx, q.topk_idx) and torch.equal(r.topk_w, q.topk_w)
         assert torch.all(mem[at + ws.nbytes:] == 77) and torch.all(mem[:at] == 0)
+
+
+def test_example_of_a_block_that_the_few_do_not_take():
+    """The example on a layer past moe_block_decode's limits, with few tokens: the operators one after another still run."""
+    import os
+    import sys
+    need_gpu()
+    say("example, inter 8200")
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import moe_block as B
+    assert B.main(["--tokens", "3", "--hidden", "64", "--inter", "8200", "--experts", "8"]) < 0.05
