@@ -694,36 +694,39 @@ hipError_t launch_adapter_down(const AdapterPass &p, hipStream_t s)
 #undef MOE_WIDE2
     }
     const size_t lds = (size_t)(waves / cw / 2) * tt * frags * 64 * 16;
-#define MOE_DOWN3(t, c, kind, v)                                                                  \
+#define MOE_DOWN4(t, c, kind, v)                                                                  \
     do {                                                                                          \
         static DevSlots slots{};                                                                  \
         const hipError_t e = lds_limit((const void *)adapter_down<t, c, kind, v>, slots, lds);    \
         if (e != hipSuccess) return e;                                                            \
         adapter_down<t, c, kind, v><<<grid, 64 * waves, lds, s>>>(p, parts, cw);                  \
     } while (0)
-#define MOE_DOWN2(t, c, kind)                                                                     \
+// large tiles of aligned rows are the kernel's above, but for codes at multiples of 8 bytes
+#define MOE_DOWN3(t, c, kind)                                                                     \
     do {                                                                                          \
-        if (vec) MOE_DOWN3(t, c, kind, true);                                                     \
-        else MOE_DOWN3(t, c, kind, false);                                                        \
+        if constexpr (t == 1 || kind == ADAPT_I8) {                                               \
+            if (vec) MOE_DOWN4(t, c, kind, true);                                                 \
+            else MOE_DOWN4(t, c, kind, false);                                                    \
+        } else MOE_DOWN4(t, c, kind, false);                                                      \
     } while (0)
-#define MOE_DOWN1(t, kind)                                                                        \
+#define MOE_DOWN2(t, kind)                                                                        \
     do {                                                                                          \
-        if (ct == 1) MOE_DOWN2(t, 1, kind);                                                       \
-        else if (ct == 2) MOE_DOWN2(t, 2, kind);                                                       \
-        else MOE_DOWN2(t, 4, kind);                                                               \
+        if (ct == 1) MOE_DOWN3(t, 1, kind);                                                       \
+        else if (ct == 2) MOE_DOWN3(t, 2, kind);                                                  \
+        else MOE_DOWN3(t, 4, kind);                                                               \
     } while (0)
 #define MOE_DOWN(t)                                                                               \
     do {                                                                                          \
-        if (p.kind == ADAPT_F32) MOE_DOWN1(t, ADAPT_F32);                                         \
-        else if (p.kind == ADAPT_BF16) MOE_DOWN1(t, ADAPT_BF16);                                  \
-        else MOE_DOWN1(t, ADAPT_I8);                                                              \
+        if (p.kind == ADAPT_F32) MOE_DOWN2(t, ADAPT_F32);                                         \
+        else if (p.kind == ADAPT_BF16) MOE_DOWN2(t, ADAPT_BF16);                                  \
+        else MOE_DOWN2(t, ADAPT_I8);                                                              \
     } while (0)
     if (tt == 1) MOE_DOWN(1);
     else MOE_DOWN(4);
-#undef MOE_DOWN1
-#undef MOE_DOWN3
 #undef MOE_DOWN
 #undef MOE_DOWN2
+#undef MOE_DOWN3
+#undef MOE_DOWN4
     return hipGetLastError();
 }
 
