@@ -129,12 +129,28 @@ __global__ __launch_bounds__(PLAN_NT) void adapter_plan(const int32_t *ids, int 
     __syncthreads();
     walk([&](int t, int b, uint64_t same) {
         const int at = mine[b] + __popcll(same & ((1ull << lane) - 1ull));
-        order[at] = t;
+        if (at < T) order[at] = t;               // ids that another stream changes between the walks
         asm volatile("" ::: "memory");
         __builtin_amdgcn_wave_barrier();
         if (same >> lane >> 1 == 0) mine[b] = at + 1;                  // the last lane moves the position on
     });
 }
+
+// ---------------------------------------------------------------- what the kernels take from a plan
+// In bounds whatever the plan's memory holds: it is the caller's, and one that is read before it is filled, or while another
+// stream fills it, may cost the results of the call but no access past its tensors.
+struct Taken { int adapter, begin, count; };     // count 0: nothing to do
+
+template <int SIZE>
+__device__ __forceinline__ Taken take_tile(const AdapterPass &p)
+{
+    const AdapterTile tile = p.tiles[blockIdx.x];
+    const int adapter = max(-1, min(tile.adapter, p.n - 1)), begin = max(0, min(tile.begin, p.T));
+    const int end = adapter < 0 ? p.T : max(0, min(p.offsets[adapter + 1], p.T));
+    return Taken{adapter, begin, adapter == tile.adapter ? max(0, min(SIZE, end - begin)) : 0};
+}
+
+__device__ __forceinline__ int token_at(const AdapterPass &p, int pos) { return (int)min((uint32_t)p.order[pos], (uint32_t)(p.T - 1)); }
 
 // ---------------------------------------------------------------- values as bf16 terms
 template <int KIND>
@@ -227,9 +243,9 @@ template <int TT, int CT, int KIND, bool VEC>
 __global__ __launch_bounds__(64 * down_waves<TT>()) void adapter_down(AdapterPass p, int k_parts, int cw)
 {
     constexpr int NS = terms<KIND>(), NW = down_waves<TT>();
-    const AdapterTile tile = p.tiles[blockIdx.x];
-    if (tile.adapter < 0) return;
-    const int end = p.offsets[tile.adapter + 1], count = min(16 * TT, end - tile.begin);
+    const Taken tile = take_tile<16 * TT>(p);
+    if (tile.adapter < 0 || tile.count == 0) return;
+    const int count = tile.count;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const int R = p.parts * p.rank, frags = (R + 15) / 16, kw = NW / cw, wc = wave % cw, wk = wave / cw;
     const int r8 = (p.rank + 7) & ~7, width = p.parts * r8;
@@ -239,7 +255,7 @@ __global__ __launch_bounds__(64 * down_waves<TT>()) void adapter_down(AdapterPas
     const void *row[TT];
 #pragma unroll
     for (int i = 0; i < TT; ++i) {
-        const int t = p.order[tile.begin + min(16 * i + r, count - 1)];
+        const int t = token_at(p, tile.begin + min(16 * i + r, count - 1));
         row[i] = (const char *)p.x + (int64_t)t * p.ldx * (KIND == ADAPT_F32 ? 4 : KIND == ADAPT_BF16 ? 2 : 1);
     }
     const uint16_t *col[CT];
@@ -369,9 +385,9 @@ template <int TT, bool BF16, bool VEC, int KS>   // KS: steps of 32 of the rank
 __global__ __launch_bounds__(256) void adapter_up(AdapterPass p, int k_parts, int chunks)
 {
     __shared__ bf16x8 low[3][TT][KS][64];
-    const AdapterTile tile = p.tiles[blockIdx.x];
-    if (tile.adapter < -1 || (tile.adapter < 0 && p.add == p.y)) return;
-    const int end = tile.adapter < 0 ? p.T : p.offsets[tile.adapter + 1], count = min(16 * TT, end - tile.begin);
+    const Taken tile = take_tile<16 * TT>(p);
+    if (tile.count == 0 || (tile.adapter < 0 && p.add == p.y)) return;
+    const int count = tile.count;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
     const int Np = p.N / p.parts, groups = (Np + WIDE - 1) / WIDE, r8 = (p.rank + 7) & ~7, width = p.parts * r8;
     const int q = blockIdx.y / chunks, chunk = blockIdx.y % chunks, u1 = groups * (chunk + 1) / chunks;
@@ -380,7 +396,7 @@ __global__ __launch_bounds__(256) void adapter_up(AdapterPass p, int k_parts, in
 #pragma unroll
     for (int i = 0; i < TT; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) t[i][e] = p.order[tile.begin + min(16 * i + 4 * g + e, count - 1)];
+        for (int e = 0; e < 4; ++e) t[i][e] = token_at(p, tile.begin + min(16 * i + 4 * g + e, count - 1));
     // what a group of 64 outputs reads: b's rows of this lane and add; the first group's are on their way while low is made.  No
     // branches: what lies past the end is clamped, and not stored; past the rank low is zero
     struct Group { u32x4 w[4][KS]; Four<BF16> old[TT][4]; };
@@ -409,7 +425,7 @@ __global__ __launch_bounds__(256) void adapter_up(AdapterPass p, int k_parts, in
         for (int i = 0; i < TT; ++i) {
             if (i % 4 != wave) continue;
             const int pos = tile.begin + min(16 * i + r, count - 1);
-            const float factor = scale * (p.x_scale ? p.x_scale[p.order[pos]] : 1.0f);
+            const float factor = scale * (p.x_scale ? p.x_scale[token_at(p, pos)] : 1.0f);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 // the parts of K in order, eight parts' loads on their way together
@@ -526,9 +542,9 @@ __global__ __launch_bounds__(256) void adapter_down_wide(AdapterPass p, int k_pa
     constexpr int XB = 64 * XROW, AB = FR * 16 * AROW, LX = XB / 4096, LA = AB < 4096 ? 1 : AB / 4096;   // loads of a wave and step
     constexpr int CW = FR >= 4 ? 4 : FR, TW = 4 / CW, CT = FR / CW, TT = 4 / TW;       // waves along columns and tokens, fragments of a wave
     extern __shared__ __align__(16) int8_t ring[];                     // [RING][x, A]
-    const AdapterTile tile = p.tiles[blockIdx.x];
-    if (tile.adapter < 0) return;
-    const int count = min(64, p.offsets[tile.adapter + 1] - tile.begin);
+    const Taken tile = take_tile<64>(p);
+    if (tile.adapter < 0 || tile.count == 0) return;
+    const int count = tile.count;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
     const int R = p.parts * p.rank, r8 = (p.rank + 7) & ~7, width = p.parts * r8;
     const int steps = (p.K + SK - 1) / SK, part = blockIdx.y;
@@ -542,7 +558,7 @@ __global__ __launch_bounds__(256) void adapter_down_wide(AdapterPass p, int k_pa
 #pragma unroll
     for (int i = 0; i < LX; ++i) {
         const int row = ((wave * LX + i) * 64 + lane) / XP, piece = (lane % XP) ^ key(row, XP);
-        xp[i] = (const char *)p.x + (int64_t)p.order[tile.begin + min(row, count - 1)] * p.ldx * ES;
+        xp[i] = (const char *)p.x + (int64_t)token_at(p, tile.begin + min(row, count - 1)) * p.ldx * ES;
         xk[i] = piece * (16 / ES);
     }
     const uint16_t *ap[LA];

@@ -524,7 +524,7 @@ size_t moe_block_decode_workspace_bytes(const moe_block *B, int T);
  * moe_adapters: x [T] rows of type MOE_ADAPT_F32, BF16 or I8 (codes, x_scale [T] then, else
  *   NULL); y and add [T] rows of type act_y (add may be y).  Where a token has no adapter, y
  *   is add, bit for bit.  The plan's three arrays are those that moe_adapter_plan filled for the
- *   same T and n_adapters: they are indices, and not checked.
+ *   same T and n_adapters; with anything else in them y is wrong, and nothing past it is touched.
  *   a: bf16 [n][parts * rank] rows lda elements apart, b: bf16 [n][out_features] rows ldb
  *   apart, both 16-byte aligned with lda and ldb multiples of 8; elements past in_features
  *   and rank up to the next multiple of 8 are read and must be zero.  scale: fp32 [n].

@@ -127,3 +127,45 @@ def test_block_step_with_adapters_of_a_chunk():
     shared = h @ (d(wd) * d(sd)[:, None]).t()
     want, bound = adapters_reference(*down, 1, ids, h, d(routed) + shared, F32)
     assert torch.all((d(y) - want).abs() <= bound + 8 * H24 * (shared.abs() + d(routed).abs()))
+
+
+@pytest.mark.parametrize("T,kind", [(40, BF16), (513, BF16), (600, "i8"), (577, F32), (530, "odd")])
+def test_adapters_plan_of_anything(T, kind):
+    """Plans that hold anything (read while another stream fills them, say): what lies around y, add and the workspace stays as
+    it was, and so does what the call reads; the next call with a plan of its own is right."""
+    need_gpu()
+    K, N, r, parts, n = (1001 if kind == "odd" else 1008), 192, 16, 2, 5
+    a, b, scale = make_adapters(7, n, K, N, r, parts)
+    w = M.AdapterWeights(a.cuda(), b.cuda(), scale.cuda(), parts)
+    g = torch.Generator().manual_seed(T)
+    x = torch.randint(-127, 128, (T, K), generator=g).to(torch.int8) if kind == "i8" else rnd(3, T, K, dtype=F32 if kind == "odd" else kind)
+    xs = torch.full((T,), 0.01) if kind == "i8" else None
+    xd, xsd = x.cuda(), None if xs is None else xs.cuda()
+    room = torch.full((T + 256, N), 77.0, device="cuda")
+    y, size = room[128:128 + T], w.workspace(T).nbytes
+    mem = torch.full((size + 65536,), 77, dtype=torch.uint8, device="cuda")
+    ws = mem[32768:32768 + size]
+
+    def ints(lo, hi, *shape):
+        return torch.randint(lo, hi, shape, generator=g).int().cuda()
+
+    for i in range(8):
+        plan, far = M.AdapterPlan(T, n), 2 ** 31 - 1 if i % 2 else T + 70
+        plan.order, plan.offsets = ints(-far, far, T), ints(-far, far, n + 1)
+        plan.tiles = torch.stack([ints(-3, n + 3, len(plan.tiles)), ints(-far, far, len(plan.tiles))], 1).contiguous()
+        if i == 7:
+            plan.tiles[:, 0] = ints(-2 ** 31, 2 ** 31 - 1, len(plan.tiles))
+        say("adapters, a plan of anything", T, kind, i)
+        M.adapters(w, plan, xd, xsd, y, None, ws)
+        torch.cuda.synchronize()
+        assert torch.all(room[:128] == 77) and torch.all(room[128 + T:] == 77)
+        assert torch.all(mem[:32768] == 77) and torch.all(mem[32768 + size:] == 77)
+    add = rnd(5, T, N)
+    y.copy_(add)
+    ids = torch.randint(-1, n, (T,), generator=g).int()
+    M.adapter_plan(ids.cuda(), plan)
+    M.adapters(w, plan, xd, xsd, y, None, ws)
+    torch.cuda.synchronize()
+    value = x.double() if xs is None else x.double() * xs.double()[:, None]
+    want, bound = adapters_reference(a, b, scale, parts, ids, value, add, F32)
+    assert torch.all((y.double().cpu() - want).abs() <= bound)
