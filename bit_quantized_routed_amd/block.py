@@ -82,7 +82,9 @@ class MoeBlock:
 
     def decode(self, x, residual, b: BlockBuffers, stream=None):
         """The block for up to 16 tokens in two kernels (see moe_block_decode).  x, residual: [T, H] rows; residual is updated in
-        place.  Returns b.y.  Buffers that may be in use at the same time need a BlockBuffers each."""
+        place.  Returns b.y, and b.routing is filled (n and what lies between stay in the kernels).  Buffers that may be in use
+        at the same time need a BlockBuffers each.  Faster than __call__ for every batch that it takes: of the full layer (7168
+        features, experts of 2048, 8 of 256) 1 token 56 us (66), 4 122 (190), 8 234 (391), 16 412 (560)."""
         if b.ws_few is None:
             raise ValueError("decode takes up to %d tokens of a CB2 / Q2_K layer, of at most 8192 features, 512 experts and top 16"
                              % FEW_TOKENS)

@@ -27,6 +27,10 @@ struct AdapterPass {
     float *low;                                  // workspace: [parts of K][T, in the plan's order][parts][rank up to a multiple of 8]
 };
 
+// Small tiles waste fewer rows where an adapter has few tokens, large ones read its matrices less often.  512 tokens take 17 to 19 us in
+// tiles of 16 and 20 to 26 in tiles of 64 (7168 -> 4096 with rank 2 x 16 and codes of 2048 -> 7168 with rank 32), with rank 2 x 64 33
+// and 34 to 49; 2048 tokens 33 to 38 and 32 to 41, with rank 2 x 64 68 to 74 and 43 to 47.  Between them it hangs on the adapters:
+// 1024 tokens 22 to 26 and 28 to 31, with rank 2 x 64 39 and 46 (8 adapters in runs) or 50 and 40 (32, mixed).
 inline int adapter_tile(int T) { return T <= 512 ? 16 : 64; }
 // at most so many tiles, with those of tokens without an adapter
 inline int adapter_tiles(int T, int n) { return T / adapter_tile(T) + (T < n + 1 ? T : n + 1); }

@@ -234,7 +234,7 @@ __device__ __forceinline__ void as_terms(const Raw &v, bf16x8 t[3])
 // share out the columns of low (cw ways, up to CT fragments each) and what is left of
 // the split the part's K, in stretches of whole steps of 64 (a line of 128 bytes of
 // bf16, requested at once; neighbouring waves are on different L2 channels); these
-// sums meet in LDS in a fixed order.  64 tokens of 16 adapters, 7168 in, rank 2 x 32: 6 us.
+// sums meet in LDS in a fixed order.  64 tokens of 32 adapters, 7168 in, rank 2 x 16: 6 us.
 template <int TT>
 constexpr int down_waves() { return TT == 1 ? 8 : 4; }
 constexpr int DSTEP = 64;

@@ -21,8 +21,11 @@
 // int8 digits, so that dot products with integer weights run on the int8 matrix
 // instructions exactly: CB2's s_j C and Q2_K's sc_j q are at most 45, the shared
 // expert's weights are int8 as they are.  A block's sums leave as fp32, times its
-// scales, and are added in fp32.  The one rounding of the activations is 2^-24 of
-// their block's largest value, as fine as fp32's own for that value.
+// scales, and are added in fp32.  An activation is off by at most 1.5 units of its
+// block's largest value / (127 * 2^16), 1.8e-7 of that value (half a unit for the
+// integer, the rest for the reciprocal and the product before it), and its scale by
+// an fp32 rounding.  A block whose largest value is below 2^-100 counts as zero: its
+// reciprocal would not be finite.
 //
 // A lane streams a quantized block of its own (a row's four consecutive blocks are
 // read by one load, lanes r + 16 g, g = 0..3); the matrix instruction's 16 rows are
@@ -33,14 +36,16 @@
 // What bounds it.  Its floor is the weights of the experts that the tokens chose,
 // but the parts stand in a row and each has its latency: one token, H 7168, I 2048,
 // 8 of 256 experts and a shared one, 125 MB: 50 us (2.5 TB/s; a large copy reaches
-// 5.1): 10.6 until the experts are known (the shared gate/up runs beside it), 12 of
-// routed gate/up (of that 5 more than its loads need, for the codewords' products),
-// 9 until every h is there, 9 of rows of y, and the drain.  Four such tokens, 332 MB:
-// 126 us (2.6 TB/s).  Sixteen of a small layer (H 2048, I 768, 6 of 64), 60 MB: 94 us,
-// bound by the arithmetic, which is done for each pair of a token and an expert.  The
-// norm before it: 7, 12 and 9 us.  One work-group a CU of eight waves, because the
-// tables and digits take most of the LDS and the products up to 256 registers (the
-// same with 12 waves 65 us and with 16, which spill, 80, when this took 62).
+// 5.1): 10 until the experts are known (the shared gate/up runs beside it), 10 of
+// routed gate/up (6 without its arithmetic, 8 without its loads), 9 until every h is
+// there, 9 of rows of y, and the drain.  Four such tokens, 332 MB: 127 us (2.6 TB/s;
+// the SIMDs issue vector instructions 44% of the time).  Sixteen of a small layer (H
+// 2048, I 768, 6 of 64), 60 MB: 95 us, of which the rows of y are 41, on half of the
+// CUs and in six passes over h, and the routed gate/up 10 to 25, whose tokens' digits
+// are staged for every pair (vector instructions 23% of the time).  The norm before
+// it: 7, 12 and 9 us.  One work-group a CU of eight waves, because the tables and
+// digits take most of the LDS and the products up to 256 registers (the same with 12
+// waves 65 us and with 16, which spill, 80, when this took 62).
 #include "block.h"
 #include "common.h"
 #include "devcache.h"
@@ -970,6 +975,8 @@ void block_layout(BlockPass &p)
     p.nb = up(p.H, 256); p.nq = up(p.nb, 4);
     p.nbi = up(p.I, 256); p.nqi = up(p.nbi, 4);
     p.nbs = up(p.sh, 256); p.nqs = up(p.nbs, 4);
+    // an item's units are F / 16 * nq, for eight waves: of wide rows 64 features are enough (7168: one token 55 us and four 130, with
+    // 128 features 62 and 129, eight 236 and 226), of narrow ones 128 (sixteen tokens of 2048: 101 us, with 64 features 104)
     p.F = p.nq >= 4 ? 64 : 128;
     p.nf = up(p.I, p.F);
     p.records = p.nf * p.F / 64;
@@ -978,6 +985,8 @@ void block_layout(BlockPass &p)
     p.experts = std::max(1, up(p.E * p.T, 256));
     p.t_shared = up(p.sh, 8);
     p.t_down = up(p.H, p.rows);
+    // four tokens' digits are the 16 rows of an instruction, and at 8192 features all of the LDS that is left (with two tokens, four of
+    // 7168 take 143 us, not 130, and sixteen of 2048 112, not 101)
     p.slots = std::min(p.T, 4);
     // LDS: table, zeros, planes (or rows of h), scales, sums
     const int units = p.F / 16 * p.nq;

@@ -477,10 +477,11 @@ size_t moe_linear_i8_workspace_bytes(const moe_linear *W, int T);
  *     the routing of n               as moe_route_scored, its outputs written
  *     y = sum_j topk_w[j] * FFN_{topk_idx[j]}(n) + FFN_shared(n)       fp32 [T] rows, ldy apart
  * where it stands for moe_residual_norm, moe_route_scored, moe_expert_ffn_decode and the
- * shared expert's int8 linear layers.  Weights are applied exactly and activations with an
- * error of 2^-24 of the largest value of their 256 neighbours, sums are exact within 256
- * products and fp32 beyond: y is within about 4e-7 (2-norm) of 64-bit arithmetic on the
- * same n.  The shared expert's activations are not cut to 8 bits here, so its output
+ * shared expert's int8 linear layers.  Weights are applied exactly, activations with an
+ * error of at most 1.5 / (127 * 2^16) of the largest value of their block of 256 (64 in a
+ * routed expert's h), sums are exact within a block and fp32 beyond: y is within about 4e-7
+ * (2-norm) of 64-bit arithmetic on the same n.  A block whose largest value is below 2^-100
+ * counts as zero, as does silu of a gate below -88.  The shared expert's activations are not cut to 8 bits here, so its output
  * differs from that of moe_linear_i8 on codes by those codes' rounding.  A token's y
  * depends on the rest of the batch only in the order of fp32 sums.
  *   B->norm, B->router, B->layer: as in their own calls; the layer without a shared expert of
@@ -533,7 +534,7 @@ size_t moe_block_decode_workspace_bytes(const moe_block *B, int T);
  *   rows of 16-byte aligned pieces run fastest.  fp32 inputs go as three bf16 terms that add
  *   up to them, products and terms are exact; values past 3.38e38 or infinite give NaN.
  *   Workspace: moe_adapters_workspace_bytes() (0 if W is invalid), for every batch of up to T
- *   tokens, 16-byte aligned, no clearing. */
+ *   tokens, 16-byte aligned, no clearing; calls that may overlap in time need one each. */
 enum moe_adapt_x { MOE_ADAPT_F32 = 0, MOE_ADAPT_BF16 = 1, MOE_ADAPT_I8 = 2 };
 typedef struct moe_adapter_set {
     int32_t in_features, out_features, n_adapters, rank, parts;
